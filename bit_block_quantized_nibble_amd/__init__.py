@@ -1,6 +1,8 @@
 """Python binding of libqbn: fused dequantize-and-dot over packed 4-bit
 block-quantized weights (MXFP4, NVFP4, Q4_K), bulk dequantization of six
-formats and bit-exact int4 layout repacks, on AMD MI355X (gfx950).
+formats and bit-exact int4 layout repacks, on AMD MI355X (gfx950). The paged
+key-value cache that a decode step streams next to the weights (append,
+attention, page bookkeeping) is bound in kv.py and exported from here.
 
 This module only marshals arguments: it checks that every tensor is a
 device tensor holding at least the bytes the call will touch (the C ABI
@@ -23,7 +25,8 @@ import torch
 __all__ = [
     "QTensor", "QbnError", "RepackRefused", "quantized_gemv", "quantized_gemm", "dequantize", "repack", "validate",
     "validate_async", "nbytes", "status_string", "lib_path", "FORMATS", "Prepared", "prepare_gemv", "prepare_gemm",
-    "prepare_dequantize", "prepare_repack",
+    "prepare_dequantize", "prepare_repack", "KVCache", "KVPool", "kv_append", "kv_attention_decode",
+    "kv_attention_prefill", "kv_reserve", "kv_fork", "kv_free", "kv_compact", "kv_nbytes",
 ]
 
 FORMATS = {"mxfp4": 1, "nvfp4": 2, "q4_k": 3, "q4_0": 4, "gptq4": 5, "awq4": 6, "nvfp4_cke": 8}
@@ -709,3 +712,7 @@ def prepare_repack(src: QTensor, dst: QTensor, status: torch.Tensor) -> Prepared
     cs, cd = src._c(), dst._c()
     args = (ctypes.byref(cs), ctypes.byref(cd), _ptr(status, "status"))
     return Prepared(lib.qbn_repack, args, "qbn_repack", src.device, (src, dst, status, cs, cd))
+
+
+from .kv import (KVCache, KVPool, kv_append, kv_attention_decode, kv_attention_prefill, kv_compact,  # noqa: E402
+                 kv_fork, kv_free, kv_nbytes, kv_reserve)

@@ -1,0 +1,146 @@
+// Device-side helpers of the paged key-value cache kernels (gfx950 only).
+#pragma once
+
+#include "qbn_device.h"
+#include "qbn_kv.h"
+
+namespace qbn {
+namespace kv {
+
+enum Fmt { BF16 = 0, FP8 = 1, FP4 = 2 };
+
+template <int F>
+constexpr int kBits = F == BF16 ? 16 : F == FP8 ? 8 : 4;
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// A cache of one layer as the kernels see it: bases of that layer's pages.
+struct Cache {
+    const uint8_t *k, *v, *ks, *vs;
+    int heads, page_shift;  // page_size = 1 << page_shift
+    int pages;
+};
+
+struct Batch {
+    int seqs, tokens, row;
+    int64_t row_stride;
+    const int32_t *table, *lens, *cu;
+};
+
+// E8M0 byte -> its power of two (0 -> 2^-127, a binary32 subnormal; 255 is NaN).
+__device__ __forceinline__ float e8m0_f32(uint32_t b) {
+    return __builtin_amdgcn_ldexpf(1.0f, e8m0_exponent(b));
+}
+
+// Eight consecutive elements (4, 8 or 16 bytes in w) -> bf16 pairs, exact: an
+// E2M1 or E4M3FN value has at most 4 significant bits.
+template <int F>
+__device__ __forceinline__ void expand8(const uint32_t *w, float scale, uint32_t (&o)[4]) {
+    if constexpr (F == FP4) {
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 0));
+        o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 1));
+        o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 2));
+        o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 3));
+    } else if constexpr (F == FP8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, false));
+            o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, true));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = w[i];
+    }
+}
+
+// W (2, 4 or 8) consecutive elements -> W / 2 bf16 pairs.
+template <int F, int W>
+__device__ __forceinline__ void expand(const uint32_t *w, float scale, uint32_t (&o)[W / 2]) {
+    if constexpr (W == 8) {
+        expand8<F>(w, scale, o);
+    } else if constexpr (F == FP4) {
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 0));
+        if constexpr (W == 4)
+            o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[0], scale, 1));
+    } else if constexpr (F == FP8) {
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, false));
+        if constexpr (W == 4)
+            o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, true));
+    } else {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) o[i] = w[i];
+    }
+}
+
+// Loads of 1, 2, 4, 8 or 16 bytes into 32-bit words (zero-extended).
+template <int BYTES>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+    if constexpr (BYTES == 1) {
+        w[0] = *p;
+    } else if constexpr (BYTES == 2) {
+        w[0] = *reinterpret_cast<const uint16_t *>(p);
+    } else if constexpr (BYTES == 4) {
+        w[0] = ld4(p);
+    } else if constexpr (BYTES == 8) {
+        const u32x2 t = ld8(p);
+        w[0] = t.x;
+        w[1] = t.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i) {
+            const u32x4 t = ld16(p + 16 * i);
+            w[4 * i] = t.x;
+            w[4 * i + 1] = t.y;
+            w[4 * i + 2] = t.z;
+            w[4 * i + 3] = t.w;
+        }
+    }
+}
+
+// The words of eight tokens (row j: W elements as bf16 pairs) -> for each
+// element t, the eight tokens' values as four dwords: the A operand of a
+// matrix product over tokens.
+template <int W>
+__device__ __forceinline__ u32x4 column8(const uint32_t (&c)[8][W / 2], int t) {
+    const uint32_t sel = (t & 1) ? 0x07060302u : 0x05040100u;
+    return u32x4{__builtin_amdgcn_perm(c[1][t / 2], c[0][t / 2], sel),
+                 __builtin_amdgcn_perm(c[3][t / 2], c[2][t / 2], sel),
+                 __builtin_amdgcn_perm(c[5][t / 2], c[4][t / 2], sel),
+                 __builtin_amdgcn_perm(c[7][t / 2], c[6][t / 2], sel)};
+}
+
+__device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+// v_exp_f32: 2^x within one unit in the last place, 2^-inf = 0. Results below
+// 2^-126 may come out as 0; a softmax term that small is 2^-126 of the row's
+// largest.
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Sums over the threads of a workgroup of NT threads; every thread gets the
+// sum of all threads and the sum of those before it. `lds` holds NT / 64 + 1
+// values and may be reused after the call.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *lds, int64_t &total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t s = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t t = __shfl_up(s, d);
+        if (lane >= d) s += t;
+    }
+    if (lane == 63) lds[wave] = s;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        if (w < wave) before += lds[w];
+        total += lds[w];
+    }
+    __syncthreads();
+    return before + s - v;
+}
+
+}  // namespace kv
+}  // namespace qbn

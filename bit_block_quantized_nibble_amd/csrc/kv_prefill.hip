@@ -1,0 +1,485 @@
+// Causal attention of chunks of new tokens over the paged key-value cache,
+// with a sliding window and sink tokens.
+//
+// The rows of a workgroup are (token, query head) pairs of one key-value head:
+// heads that share K and V share the loads and the expansion to bf16, and a
+// chunk of a few tokens still fills rows. K and V go through LDS in tiles of
+// 64 tokens, two buffers, the next tile's bytes in registers while this one
+// is computed; K as [token][head_dim] with 16 bytes of padding, V transposed
+// ([head_dim][token], 16-byte pieces swizzled), so that both operands of both
+// products are 16-byte LDS reads without bank conflicts.
+//
+// As in the decode kernel the products are transposed: S^T = K Q^T with the
+// rows of K permuted so that a lane's scores are exactly the eight tokens per
+// step that it supplies to out^T = V^T P^T. A lane owns one row: the softmax
+// needs no cross-lane work but one exchange between the two halves of a wave,
+// and only when a score exceeds the running reference by 2^8.
+//
+// Bound by the matrix cores together with the exponentials and LDS reads.
+#include "kv_device.h"
+#include "kv_launch.h"
+
+namespace qbn {
+namespace {
+
+using namespace kv;
+
+constexpr int BN = 64;  // tokens per tile
+
+struct PrefillArgs {
+    Cache c;
+    Batch b;
+    const __bf16 *q;
+    int64_t qt, qh;
+    __bf16 *out;
+    float *lse;
+    float *parts;  // [splits][tokens][heads][D] sums, then [splits][tokens][heads] references and weight sums
+    float scale;   // times log2 e
+    int group, window, sinks, splits, dim;
+};
+
+template <int F, int D, int NW>
+struct Lay {
+    static constexpr int NT = NW * 64, BM = NW * 32;
+    static constexpr int KROW = 2 * D + 16;         // bytes of a K row in LDS
+    static constexpr int VOFF = BN * KROW;
+    static constexpr int BUF = VOFF + D * 2 * BN;   // one buffer
+    static constexpr int HALF = 2 * D;              // K items (32 elements of a token); as many V items (4 x 8 tokens)
+    static constexpr int ITEMS = (2 * HALF + NT - 1) / NT;
+    static constexpr int KW = kBits<F>;             // words of a K item
+    static constexpr int VW = F == BF16 ? 2 : 1;    // words of a V item's token
+    static constexpr int RAW = (KW > 8 * VW ? KW : 8 * VW);
+};
+
+__device__ __forceinline__ int v_swizzle(int d) { return ((d >> 1) ^ (d >> 4)) & 7; }
+
+// A sequence's new tokens, as far as cu is in order and inside q.
+__device__ __forceinline__ int new_tokens(const Batch &b, int s, int &first) {
+    if (!b.cu) {
+        first = s;
+        return 1;
+    }
+    const int x = b.cu[s], y = b.cu[s + 1];
+    first = x;
+    return x >= 0 && y >= x && y <= b.tokens ? y - x : 0;
+}
+
+// One element of V, as the tiles see it.
+template <int F, int D>
+__device__ __forceinline__ float element(const Cache &c, int64_t head, int ps, int slot, int d) {
+    const int64_t at = (head * ps + slot) * D + d;
+    uint32_t w[2] = {0, 0}, o[1];
+    if constexpr (F == BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(c.v)[at] << 16);
+    if constexpr (F == FP8) w[0] = c.v[at];
+    if constexpr (F == FP4) w[0] = (c.v[at / 2] >> (4 * (d & 1))) & 15u;
+    expand<F == BF16 ? FP8 : F, 2>(w, e8m0_f32(c.vs[(head * (D / 32) + d / 32) * ps + slot]), o);
+    return __uint_as_float(o[0] << 16);
+}
+
+template <int F, int D, int NW>
+__global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a) {
+    using L = Lay<F, D, NW>;
+    __shared__ __align__(16) uint8_t s_buf[2][L::BUF];
+    __shared__ int s_odd;  // a tile that not every row sees held an infinity or NaN of V
+    __shared__ int64_t s_scan[NW + 1];
+    __shared__ int s_at[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 31, half = lane >> 5;
+    const int kv_head = blockIdx.x % a.c.heads;
+    const int want = blockIdx.x / a.c.heads;  // row tile in the list of all sequences'
+
+    // ---- which sequence and row tile
+    {
+        const int each = (a.b.seqs + L::NT - 1) / L::NT;
+        int64_t mine = 0;
+        int first;
+        for (int i = 0; i < each; ++i) {
+            const int s = tid * each + i;
+            if (s < a.b.seqs) mine += ((int64_t)new_tokens(a.b, s, first) * a.group + L::BM - 1) / L::BM;
+        }
+        int64_t total;
+        int64_t before = block_scan<L::NT>(mine, s_scan, total);
+        if (want >= total) return;
+        if (before <= want && want < before + mine) {
+            for (int i = 0; i < each; ++i) {
+                const int s = tid * each + i;
+                const int64_t t = ((int64_t)new_tokens(a.b, s, first) * a.group + L::BM - 1) / L::BM;
+                if (want < before + t) {
+                    s_at[0] = s;
+                    s_at[1] = (int)(before + t - 1 - want);  // the longest rows first
+                    break;
+                }
+                before += t;
+            }
+        }
+        __syncthreads();
+    }
+    const int b = __builtin_amdgcn_readfirstlane(s_at[0]), tile = __builtin_amdgcn_readfirstlane(s_at[1]);
+    int q0;
+    const int fresh = new_tokens(a.b, b, q0), rows = fresh * a.group;
+    const int r0 = tile * L::BM;
+    int len = a.b.lens[b];
+    const int ps = 1 << a.c.page_shift;
+    bool bad = len < 0 || (((int64_t)len + ps - 1) >> a.c.page_shift) > a.b.row;
+    if (bad) len = 0;
+    // this lane's row; rows beyond the last repeat it and are not written
+    const int r = r0 + wave * 32 + n;
+    const bool mine = r < rows;
+    const int rr = mine ? r : rows - 1, qi = rr / a.group, head = kv_head * a.group + rr % a.group;
+    const int pos = len - fresh + qi;
+    const int pmin = len - fresh + r0 / a.group;
+    const int pmax = len - fresh + (min(r0 + L::BM, rows) - 1) / a.group;
+    // keys that some row of the workgroup sees: the sinks, then from lo to pmax
+    const int lo = a.window > 0 && pmin >= a.window ? pmin - a.window + 1 : 0;
+    const int first = lo / BN, sink_tiles = min((min(a.sinks, lo) + BN - 1) / BN, first);
+    const int all = bad || pmax < 0 ? 0 : sink_tiles + pmax / BN + 1 - first;
+    const int u0 = (int)((int64_t)all * blockIdx.y / a.splits), u1 = (int)((int64_t)all * (blockIdx.y + 1) / a.splits);
+
+    bf16x8 q[D / 16];
+    {
+        const __bf16 *row = a.q + (int64_t)(q0 + qi) * a.qt + (int64_t)head * a.qh + 8 * half;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) q[k] = as_bf16x8(ld16(row + 16 * k));
+    }
+    f32x16 acc[D / 32];
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
+    float ref = kNegInf, sum = 0.0f;
+
+    const auto tile_token = [&](int u) { return (u < sink_tiles ? u : u - sink_tiles + first) * BN; };
+    // tokens that every row of the workgroup sees need no mask
+    const auto is_edge = [&](int t0) {
+        return t0 + BN - 1 > pmin || (a.window > 0 && t0 <= pmax - a.window && t0 + BN > a.sinks);
+    };
+    const auto is_seen = [&](int t) { return t <= pmax && (t >= lo || t < a.sinks); };
+
+    uint32_t raw[L::ITEMS][L::RAW];
+    u32x2 rsc[L::ITEMS];
+    const auto load = [&](int t0) {
+        int page[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 16 * i;
+            const bool any = t <= pmax && (t + 15 >= lo || t < a.sinks);
+            int p = 0;
+            if (any) p = a.b.table[(int64_t)b * a.b.row_stride + (t >> a.c.page_shift)];
+            if ((uint32_t)p >= (uint32_t)a.c.pages) {
+                bad = true;
+                p = 0;
+            }
+            page[i] = p;
+        }
+        const auto base_of = [&](int t) {
+            const int i = t >> 4;
+            const int p = i < 2 ? (i == 0 ? page[0] : page[1]) : (i == 2 ? page[2] : page[3]);
+            return (int64_t)p * a.c.heads + kv_head;
+        };
+#pragma unroll
+        for (int i = 0; i < L::ITEMS; ++i) {
+            const int it = tid + i * L::NT;
+            if (it < L::HALF) {
+                const int t = it / (D / 32), blk = it % (D / 32), slot = (t0 + t) & (ps - 1);
+                const int64_t h = base_of(t);
+                load_words<4 * L::KW>(a.c.k + ((h * ps + slot) * D + blk * 32) * kBits<F> / 8, raw[i]);
+                if constexpr (F != BF16) rsc[i].x = a.c.ks[(h * (D / 32) + blk) * ps + slot];
+            } else if (it < 2 * L::HALF) {
+                const int v = it - L::HALF, tg = v / (D / 4), dg = v % (D / 4), slot = (t0 + 8 * tg) & (ps - 1);
+                const int64_t h = base_of(8 * tg);
+                const uint8_t *p = a.c.v + ((h * ps + slot) * D + dg * 4) * kBits<F> / 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) load_words<kBits<F> / 2>(p + j * (D * kBits<F> / 8), raw[i] + j * L::VW);
+                if constexpr (F != BF16) rsc[i] = ld8(a.c.vs + (h * (D / 32) + dg / 8) * ps + slot);
+            }
+        }
+    };
+    const auto store = [&](int t0, int buf) {
+        const bool edge = is_edge(t0);
+        uint8_t *ks = s_buf[buf], *vs = s_buf[buf] + L::VOFF;
+#pragma unroll
+        for (int i = 0; i < L::ITEMS; ++i) {
+            const int it = tid + i * L::NT;
+            if (it < L::HALF) {
+                const int t = it / (D / 32), blk = it % (D / 32);
+                const float sc = F == BF16 ? 1.0f : e8m0_f32(rsc[i].x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t o[4];
+                    expand8<F>(raw[i] + e * (L::KW / 4), sc, o);
+                    *reinterpret_cast<u32x4 *>(ks + t * L::KROW + blk * 64 + e * 16) = u32x4{o[0], o[1], o[2], o[3]};
+                }
+            } else if (it < 2 * L::HALF) {
+                const int v = it - L::HALF, tg = v / (D / 4), dg = v % (D / 4);
+                uint32_t c[8][2];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float sc = F == BF16 ? 1.0f : e8m0_f32((j < 4 ? rsc[i].x : rsc[i].y) >> (8 * (j & 3)));
+                    expand<F, 4>(raw[i] + j * L::VW, sc, c[j]);
+                }
+                if (edge) {  // what no row sees becomes 0; what only some see is looked over
+                    bool odd = false;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const bool on = is_seen(t0 + 8 * tg + j);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            c[j][k] = on ? c[j][k] : 0u;
+                            odd |= (c[j][k] & 0x7F80u) == 0x7F80u || (c[j][k] & 0x7F800000u) == 0x7F800000u;
+                        }
+                    }
+                    if (__any(odd)) {  // taken out of the product; add_special puts them where they belong
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                c[j][k] &= (c[j][k] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
+                                c[j][k] &= (c[j][k] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : 0xFFFFFFFFu;
+                            }
+                        s_odd = 1;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = dg * 4 + e;
+                    *reinterpret_cast<u32x4 *>(vs + d * (2 * BN) + ((tg ^ v_swizzle(d)) * 16)) = column8<4>(c, e);
+                }
+            }
+        }
+    };
+
+    const int krow = 16 * (n / 16) + 8 * (n / 4 % 2) + 4 * (n / 8 % 2) + n % 4;  // the token of this lane's K row
+    const auto compute = [&](int t0, int buf) {
+        const uint8_t *ks = s_buf[buf], *vs = s_buf[buf] + L::VOFF;
+        f32x16 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    as_bf16x8(ld16(ks + (t * 32 + krow) * L::KROW + (16 * k + 8 * half) * 2)), q[k], s[t], 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[t][e] *= a.scale;
+        const bool edge = is_edge(t0);
+        if (edge) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int k = t0 + 32 * t + 16 * (e / 8) + 8 * half + e % 8;
+                    const bool on = k <= pos && (a.window == 0 || k > pos - a.window || k < a.sinks);
+                    s[t][e] = on ? s[t][e] : kNegInf;
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[t][e]);
+        if (__any(top > ref + 8.0f)) {
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            const float now = __builtin_fmaxf(ref, top);
+            const float f = now == ref ? 1.0f : exp2_fast(ref - now);
+            ref = now;
+            sum *= f;
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t) acc[t] *= f;
+        }
+        const float base = ref == kNegInf ? 0.0f : ref;
+        bf16x8 p[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                u32x4 w;
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const float x = exp2_fast(s[t][8 * g + j] - base), y = exp2_fast(s[t][8 * g + j + 1] - base);
+                    sum += x + y;
+                    w[j / 2] = pack_bf16x2(x, y);
+                }
+                p[2 * t + g] = as_bf16x8(w);
+            }
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) {
+            const int d = 32 * t + n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    as_bf16x8(ld16(vs + d * (2 * BN) + (((2 * i + half) ^ v_swizzle(d)) * 16))), p[i], acc[t], 0, 0, 0);
+        }
+    };
+
+    if (tid == 0) s_odd = 0;
+    __syncthreads();
+    if (u0 < u1) {
+        load(tile_token(u0));
+        store(tile_token(u0), 0);
+    }
+    __syncthreads();
+    for (int u = u0; u < u1; ++u) {
+        const int buf = (u - u0) & 1;
+        if (u + 1 < u1) load(tile_token(u + 1));
+        compute(tile_token(u), buf);
+        if (u + 1 < u1) store(tile_token(u + 1), buf ^ 1);
+        __syncthreads();
+    }
+
+    sum += __shfl_xor(sum, 32);
+    if (bad) sum = __builtin_nanf("");
+    const int64_t total = (int64_t)a.b.tokens * (a.c.heads * a.group), shift = total * blockIdx.y;
+    const int64_t row = (int64_t)(q0 + qi) * (a.c.heads * a.group) + head;
+    if (mine && a.splits == 1) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<u32x2 *>(a.out + row * D + 32 * t + 8 * i + 4 * half) =
+                    u32x2{pack_bf16x2(acc[t][4 * i] * inv, acc[t][4 * i + 1] * inv),
+                          pack_bf16x2(acc[t][4 * i + 2] * inv, acc[t][4 * i + 3] * inv)};
+        if (half == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+    } else if (mine) {
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4 *>(a.parts + (shift + row) * D + 32 * t + 8 * i + 4 * half) =
+                    f32x4{acc[t][4 * i], acc[t][4 * i + 1], acc[t][4 * i + 2], acc[t][4 * i + 3]};
+        if (half == 0) {
+            float *st = a.parts + total * a.splits * D;
+            st[shift + row] = ref;
+            st[total * a.splits + shift + row] = sum;
+        }
+    }
+    // Infinities and NaN of V in tiles that not every row sees: added to the
+    // rows that see them, after the sums are written. A thread owns an element
+    // of the head, so that no two add to the same output.
+    if (s_odd == 0) return;
+    __syncthreads();
+    for (int u = u0; u < u1; ++u) {
+        const int t0 = tile_token(u);
+        if (!is_edge(t0) || tid >= D) continue;
+        for (int t = t0; t < t0 + BN; ++t) {
+            if (!is_seen(t)) continue;
+            const int p = a.b.table[(int64_t)b * a.b.row_stride + (t >> a.c.page_shift)];
+            if ((uint32_t)p >= (uint32_t)a.c.pages) continue;
+            const int64_t h = (int64_t)p * a.c.heads + kv_head;
+            const int slot = t & (ps - 1);
+            const float v = element<F, D>(a.c, h, ps, slot, tid);
+            if (__builtin_isfinite(v)) continue;
+            const float add = __builtin_isnan(v) ? v : __builtin_copysignf(__builtin_huge_valf(), v);
+            for (int k = r0; k < min(r0 + L::BM, rows); ++k) {
+                const int pk = len - fresh + k / a.group;
+                if (t > pk || (a.window > 0 && t <= pk - a.window && t >= a.sinks)) continue;
+                const int64_t o = ((int64_t)(q0 + k / a.group) * (a.c.heads * a.group) + kv_head * a.group + k % a.group);
+                if (a.splits == 1) a.out[o * D + tid] = (__bf16)((float)a.out[o * D + tid] + add);
+                else a.parts[(shift + o) * D + tid] += add;
+            }
+        }
+    }
+}
+
+// Joins the pieces of a split length, in order: a wave per row.
+template <int D>
+__global__ __launch_bounds__(256) void k_prefill_join(PrefillArgs a, int64_t total) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= total) return;
+    const float *st = a.parts + total * a.splits * D;
+    float top = kNegInf;
+    for (int i = 0; i < a.splits; ++i) top = __builtin_fmaxf(top, st[i * total + row]);
+    constexpr int PER = (D + 63) / 64;
+    float o[PER] = {}, sum = 0.0f;
+    for (int i = 0; i < a.splits; ++i) {
+        const float ri = st[i * total + row], f = ri == top ? 1.0f : exp2_fast(ri - top);
+        sum += f * st[(a.splits + i) * total + row];
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            if (D % 64 == 0 || e * 64 + lane < D) o[e] += f * a.parts[(i * total + row) * D + e * 64 + lane];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+        if (D % 64 == 0 || e * 64 + lane < D) a.out[row * D + e * 64 + lane] = (__bf16)(o[e] * inv);
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+struct Plan {
+    int64_t tiles;  // row tiles at most
+    int splits;
+};
+
+Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
+    constexpr int BM = 128;
+    Plan p;
+    const int64_t group = q_heads / c.heads;
+    p.tiles = b.cu ? b.tokens * group / BM + b.seqs : b.seqs * ((group + BM - 1) / BM);
+    int64_t units = (b.row * c.page_size + BN - 1) / BN;
+    if (window > 0) {
+        const int64_t seen = ((int64_t)window + BM / group) / BN + 2 + ((int64_t)sinks + BN - 1) / BN;
+        if (seen < units) units = seen;
+    }
+    const int64_t blocks = p.tiles * c.heads;
+    // Few row tiles: the length is split until about two workgroups per
+    // compute unit run, each with at least eight tiles of 64 tokens.
+    int64_t splits = blocks > 0 && blocks < 512 ? 512 / blocks : 1;
+    if (splits > units / 8) splits = units / 8;
+    p.splits = (int)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+    return p;
+}
+
+template <int F>
+hipError_t launch(const PrefillArgs &a, dim3 grid, hipStream_t s) {
+    const int64_t total = (int64_t)a.b.tokens * a.c.heads * a.group;
+    const unsigned join = (unsigned)((total + 3) / 4);
+#define QBN_KV_DIM(DD)                                                         \
+    case DD:                                                                   \
+        k_prefill<F, DD, 4><<<grid, 256, 0, s>>>(a);                           \
+        if (a.splits > 1) k_prefill_join<DD><<<join, 256, 0, s>>>(a, total);   \
+        break;
+    switch (a.dim) {
+        QBN_KV_DIM(64)
+        QBN_KV_DIM(96)
+        QBN_KV_DIM(128)
+        QBN_KV_DIM(192)
+        QBN_KV_DIM(256)
+    }
+#undef QBN_KV_DIM
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t kv_prefill_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
+    const Plan p = plan_of(c, b, q_heads, window, sinks);
+    return p.splits > 1 ? p.splits * b.tokens * q_heads * ((int64_t)c.head_dim + 2) * 4 : 0;
+}
+
+hipError_t launch_kv_prefill(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, int q_heads, const KvRows &q,
+                             float scale, int window, int sinks, void *out, float *lse, void *ws, hipStream_t s) {
+    const Plan p = plan_of(c, b, q_heads, window, sinks);
+    const int64_t elems = layer * c.pages * c.heads * c.page_size * c.head_dim;
+    const int bits = c.format == QBN_KV_BF16 ? 16 : c.format == QBN_MXFP8 ? 8 : 4;
+    PrefillArgs a;
+    a.c = {(const uint8_t *)c.k + elems * bits / 8, (const uint8_t *)c.v + elems * bits / 8,
+           (const uint8_t *)c.k_scales + elems / 32, (const uint8_t *)c.v_scales + elems / 32, c.heads,
+           __builtin_ctz(c.page_size), (int)c.pages};
+    a.b = {(int)b.seqs, (int)b.tokens, (int)b.row, b.row_stride, b.table, b.lens, b.cu};
+    a.q = (const __bf16 *)q.p;
+    a.qt = q.token_stride, a.qh = q.head_stride;
+    a.out = (__bf16 *)out, a.lse = lse;
+    a.parts = (float *)ws;
+    a.scale = scale * kLog2e;
+    a.group = q_heads / c.heads, a.window = window, a.sinks = sinks, a.splits = p.splits, a.dim = c.head_dim;
+    const dim3 grid((unsigned)(p.tiles * c.heads), (unsigned)p.splits);
+    if (c.format == QBN_KV_BF16) return launch<BF16>(a, grid, s);
+    return c.format == QBN_MXFP8 ? launch<FP8>(a, grid, s) : launch<FP4>(a, grid, s);
+}
+
+}  // namespace qbn

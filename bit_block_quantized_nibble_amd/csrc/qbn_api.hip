@@ -13,17 +13,23 @@ namespace {
 
 thread_local int32_t g_last_hip_error = 0;
 
+}  // namespace
+
+int32_t qbn::hip_status(hipError_t e) {
+    if (e == hipSuccess) return QBN_OK;
+    g_last_hip_error = (int32_t)e;
+    return QBN_ERR_HIP;
+}
+
+namespace {
+
 // Largest element count a launch grid here can cover (256-thread blocks,
 // 32-bit grid dimension), with a wide margin.
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
-int32_t hip_status(hipError_t e) {
-    if (e == hipSuccess) return QBN_OK;
-    g_last_hip_error = (int32_t)e;
-    return QBN_ERR_HIP;
-}
+using qbn::hip_status;
 
 // Weight formats a qbn_tensor may carry (QBN_MXFP8 is an activation format only).
 bool known_format(int32_t f) { return (f >= QBN_MXFP4 && f <= QBN_AWQ4) || f == QBN_NVFP4_CKE; }

@@ -9,6 +9,9 @@
 
 namespace qbn {
 
+// The qbn_status of a launch; a failure is remembered for qbn_last_hip_error.
+int32_t hip_status(hipError_t e);
+
 hipError_t launch_gemv(const qbn_tensor &w, const void *x, int x_dtype, float *y, hipStream_t s);
 hipError_t launch_gemv_cke(const qbn_tensor &w, const void *x, int x_dtype, float *y, hipStream_t s);
 hipError_t launch_dequant_cke(const qbn_tensor &w, void *out, int out_dtype, int out_layout, hipStream_t s);
