@@ -12,11 +12,11 @@ from __future__ import annotations
 
 import ctypes
 import math
-from typing import Optional, Tuple
+from typing import Optional
 
 import torch
 
-from . import _check, _load, _need, _need_dtype, _stream
+from . import QbnError, _load, _need, _need_dtype
 
 KV_FORMATS = {"bf16": 16, "mxfp8": 7, "mxfp4": 1}
 KV_EXPORTED = (
@@ -25,6 +25,11 @@ KV_EXPORTED = (
     "qbn_kv_compact",
 )
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+# torch's current stream of a device as an integer: what
+# torch.cuda.current_stream(device).cuda_stream gives, without making a Stream
+# object (1.9 us of a small call's 14).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _CCache(ctypes.Structure):
@@ -83,20 +88,31 @@ def kv_nbytes(format: str, layers: int, pages: int, heads: int, page_size: int, 
     return int(_kv().qbn_kv_bytes(KV_FORMATS[format], layers, pages, heads, page_size, head_dim, part))
 
 
-def _same_device(first: torch.Tensor, *others: Tuple[Optional[torch.Tensor], str]):
-    if not first.is_cuda:
-        raise ValueError("the cache's tensors must be device (cuda) tensors")
-    for t, name in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, first.device))
+# The checks below run before every call, next to kernels of a few
+# microseconds: they compare device indexes and types without building
+# objects, and leave the words to the branch that raises.
+
+def _elsewhere(t: torch.Tensor, name: str):
+    raise ValueError("%s is on %s, the cache or pool on another device" % (name, t.device))
 
 
-def _ints(t: torch.Tensor, n: int, name: str):
-    _need_dtype(t, (torch.int32,), name)
-    if t.dim() != 1 or (n > 1 and t.stride(0) != 1):
+def _first_device(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("the tensors of a cache or pool must be device (cuda) tensors")
+    return t.get_device()
+
+
+def _ints(t: torch.Tensor, n: int, dev: int, name: str) -> int:
+    """The address of an int32 vector of n entries on device dev."""
+    if t.dtype is not _I32:
+        _need_dtype(t, (_I32,), name)
+    if t.dim() != 1 or not t.is_contiguous():
         raise ValueError("%s must be a contiguous vector" % name)
-    if t.shape[0] != n:
-        raise ValueError("%s has %d entries; the call needs %d" % (name, t.shape[0], n))
+    if t.numel() != n:
+        raise ValueError("%s has %d entries; the call needs %d" % (name, t.numel(), n))
+    if t.get_device() != dev:
+        _elsewhere(t, name)
+    return t.data_ptr()
 
 
 class KVCache:
@@ -134,10 +150,13 @@ class KVCache:
             _need_dtype(t, (dt if name in ("k", "v") else torch.uint8,), name)
             if not t.is_contiguous():
                 raise ValueError("%s must be contiguous" % name)
-        _same_device(k, *parts)
+        self.index = _first_device(k)
+        for t, name in parts:
+            if t.get_device() != self.index:
+                _elsewhere(t, name)
         self.format, self.k, self.v, self.k_scales, self.v_scales = format, k, v, k_scales, v_scales
         self.layers, self.pages, self.heads, self.page_size, self.head_dim = layers, pages, heads, page, dim
-        self.device = k.device
+        self.device, self.scale = k.device, 1.0 / math.sqrt(dim)
         self._c = _CCache(KV_FORMATS[format], heads, dim, page, layers, pages, k.data_ptr(), v.data_ptr(),
                           k_scales.data_ptr() if k_scales is not None else None,
                           v_scales.data_ptr() if v_scales is not None else None)
@@ -165,16 +184,15 @@ class KVPool:
     the page; 0 is free)."""
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int):
-        _need_dtype(table, (torch.int32,), "table")
+        _need_dtype(table, (_I32,), "table")
         if table.dim() != 2 or not table.is_contiguous():
             raise ValueError("table must be a contiguous [seqs][row] matrix")
-        _ints(lens, table.shape[0], "lens")
-        _ints(refs, refs.numel(), "refs")
-        _same_device(table, (lens, "lens"), (refs, "refs"))
+        self.index = _first_device(table)
+        seqs, row = table.shape
         self.table, self.lens, self.refs, self.page_size = table, lens, refs, int(page_size)
-        self.device = table.device
-        self._c = _CPool(table.shape[0], table.shape[1], refs.shape[0], self.page_size, 0, table.data_ptr(),
-                         lens.data_ptr(), refs.data_ptr())
+        pages = refs.numel()
+        self._c = _CPool(seqs, row, pages, self.page_size, 0, table.data_ptr(), _ints(lens, seqs, self.index, "lens"),
+                         _ints(refs, pages, self.index, "refs"))
         self._ref = ctypes.byref(self._c)
 
     @classmethod
@@ -191,29 +209,38 @@ class KVPool:
                    other.page_size)
 
 
-def _batch(cache: KVCache, tokens: int, table: torch.Tensor, lens: torch.Tensor, cu: Optional[torch.Tensor]) -> _CBatch:
-    _need_dtype(table, (torch.int32,), "table")
-    if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+def _batch(dev: int, tokens: int, table: torch.Tensor, lens: torch.Tensor, cu: Optional[torch.Tensor]) -> _CBatch:
+    if table.dtype is not _I32:
+        _need_dtype(table, (_I32,), "table")
+    if table.dim() != 2:
         raise ValueError("table must be [seqs][row] with contiguous rows")
     seqs, row = table.shape
-    _ints(lens, seqs, "lens")
-    stride = table.stride(0) if seqs > 1 else row
+    if table.is_contiguous():
+        stride = row
+    else:
+        if row > 1 and table.stride(1) != 1:
+            raise ValueError("table must be [seqs][row] with contiguous rows")
+        stride = table.stride(0) if seqs > 1 else row
+    if table.get_device() != dev:
+        _elsewhere(table, "table")
     if cu is None:
         if tokens != seqs:
             raise ValueError("%d tokens for %d sequences: one each is wanted without cu" % (tokens, seqs))
-    else:
-        _ints(cu, seqs + 1, "cu")
-    _same_device(cache.k, (table, "table"), (lens, "lens"), (cu, "cu"))
-    return _CBatch(seqs, tokens, row, stride, table.data_ptr(), lens.data_ptr(), None if cu is None else cu.data_ptr())
+        return _CBatch(seqs, tokens, row, stride, table.data_ptr(), _ints(lens, seqs, dev, "lens"), None)
+    return _CBatch(seqs, tokens, row, stride, table.data_ptr(), _ints(lens, seqs, dev, "lens"),
+                   _ints(cu, seqs + 1, dev, "cu"))
 
 
-def _vectors(t: torch.Tensor, heads: int, dim: int, name: str):
+def _vectors(t: torch.Tensor, heads: int, dim: int, dev: int, name: str):
     """Strides of [tokens][heads][dim] vectors (views are taken as they are)."""
     if t.dim() != 3 or t.shape[2] != dim or (heads and t.shape[1] != heads):
         raise ValueError("%s must be [tokens][%s][%d], got %s" % (name, heads or "heads", dim, tuple(t.shape)))
-    if t.stride(2) != 1:
+    a, b, c = t.stride()
+    if c != 1:
         raise ValueError("the last axis of %s must be contiguous" % name)
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    if t.get_device() != dev:
+        _elsewhere(t, name)
+    return a if t.shape[0] > 1 else 0, b if t.shape[1] > 1 else 0
 
 
 def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -222,49 +249,65 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, table: torch.Ten
     their pages. lens int32 [seqs] counts each sequence's tokens INCLUDING the
     new ones; cu int32 [seqs + 1] says which rows of k and v are whose (None: one
     new token per sequence). MX formats are quantized as quantize_mx does."""
-    lib = _kv()
-    ks, vs = _vectors(k, cache.heads, cache.head_dim, "k"), _vectors(v, cache.heads, cache.head_dim, "v")
-    _need_dtype(k, (torch.float32, torch.bfloat16), "k")
-    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+    lib, dev = _bound or _kv(), cache.index
+    kt, kh = _vectors(k, cache.heads, cache.head_dim, dev, "k")
+    vt, vh = _vectors(v, cache.heads, cache.head_dim, dev, "v")
+    dtype, tokens = _DTYPES.get(k.dtype), k.shape[0]
+    if dtype is None:
+        _need_dtype(k, (torch.float32, torch.bfloat16), "k")
+    if v.dtype is not k.dtype or v.shape[0] != tokens:
         raise ValueError("k and v must be alike")
-    _same_device(cache.k, (k, "k"), (v, "v"))
-    b = _batch(cache, k.shape[0], table, lens, cu)
-    _check(lib.qbn_kv_append(cache._ref, layer, ctypes.byref(b), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
-                             vs[1], _DTYPES[k.dtype], _stream(cache.device)), "qbn_kv_append")
+    b = _batch(dev, tokens, table, lens, cu)
+    st = lib.qbn_kv_append(cache._ref, layer, b, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dtype, _raw_stream(dev))
+    if st:
+        raise QbnError(st, "qbn_kv_append")
 
 
 def _attention(decode: bool, cache, q, cu, table, lens, window, sinks, scale, layer, out, lse, workspace):
-    lib = _kv()
-    qs = _vectors(q, 0, cache.head_dim, "q")
-    _need_dtype(q, (torch.bfloat16,), "q")
-    tokens, heads = q.shape[0], q.shape[1]
-    b = _batch(cache, tokens, table, lens, cu)
-    dev = cache.device
+    lib, dev, dim = _bound or _kv(), cache.index, cache.head_dim
+    qt, qh = _vectors(q, 0, dim, dev, "q")
+    if q.dtype is not _BF16:
+        _need_dtype(q, (_BF16,), "q")
+    tokens, heads, _ = shape = q.shape
+    b = _batch(dev, tokens, table, lens, cu)
     if out is None:
-        out = torch.empty((tokens, heads, cache.head_dim), dtype=torch.bfloat16, device=dev)
-    elif out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be contiguous [tokens][heads][head_dim]")
-    if lse is None:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
-    elif lse.shape != q.shape[:2] or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous [tokens][heads]")
-    _need_dtype(out, (torch.bfloat16,), "out")
-    _need_dtype(lse, (torch.float32,), "lse")
-    need = lib.qbn_kv_attention_workspace(cache._ref, ctypes.byref(b), heads, window, sinks, int(decode))
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+        out = q.new_empty(shape)
     else:
-        _need(workspace, need, "workspace")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    _same_device(cache.k, (q, "q"), (out, "out"), (lse, "lse"), (workspace, "workspace"))
+        if out.shape != shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous [tokens][heads][head_dim]")
+        _need_dtype(out, (_BF16,), "out")
+        if out.get_device() != dev:
+            _elsewhere(out, "out")
+    if lse is None:
+        lse = q.new_empty((tokens, heads), dtype=_F32)
+    else:
+        if lse.shape != shape[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous [tokens][heads]")
+        _need_dtype(lse, (_F32,), "lse")
+        if lse.get_device() != dev:
+            _elsewhere(lse, "lse")
+    need = lib.qbn_kv_attention_workspace(cache._ref, b, heads, window, sinks, decode)
+    ws = None
+    if workspace is not None:
+        ws, need = _given_workspace(workspace, need, dev)
+    elif need > 0:
+        workspace = q.new_empty(need, dtype=torch.uint8)
+        ws = workspace.data_ptr()
     fn = lib.qbn_kv_attention_decode if decode else lib.qbn_kv_attention_prefill
-    _check(fn(cache._ref, layer, ctypes.byref(b), heads, q.data_ptr(), qs[0], qs[1],
-              1.0 / math.sqrt(cache.head_dim) if scale is None else scale, window, sinks, out.data_ptr(),
-              lse.data_ptr(), workspace.data_ptr() if workspace is not None else None,
-              workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(dev)),
-           "qbn_kv_attention_decode" if decode else "qbn_kv_attention_prefill")
+    st = fn(cache._ref, layer, b, heads, q.data_ptr(), qt, qh, cache.scale if scale is None else scale, window, sinks,
+            out.data_ptr(), lse.data_ptr(), ws, need, _raw_stream(dev))
+    if st:
+        raise QbnError(st, "qbn_kv_attention_decode" if decode else "qbn_kv_attention_prefill")
     return out, lse
+
+
+def _given_workspace(t: torch.Tensor, need: int, dev: int):
+    _need(t, need, "workspace")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if t.get_device() != dev:
+        _elsewhere(t, "workspace")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def kv_attention_decode(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, window: int = 0,
@@ -289,28 +332,28 @@ def kv_attention_prefill(cache: KVCache, q: torch.Tensor, cu: Optional[torch.Ten
     return _attention(False, cache, q, cu, table, lens, window, sinks, scale, layer, out, lse, workspace)
 
 
-def _pools(pool: KVPool, out: Optional[KVPool], cache: Optional[KVCache] = None):
+def _out(pool: KVPool, out: Optional[KVPool], cache: Optional[KVCache] = None) -> KVPool:
     out = pool if out is None else out
-    _same_device(pool.table, (out.table, "out"), (cache.k if cache is not None else None, "cache"))
+    if out.index != pool.index:
+        _elsewhere(out.table, "out")
+    if cache is not None and cache.index != pool.index:
+        _elsewhere(pool.table, "pool")
     return out
 
 
 def _pool_workspace(lib, pool: KVPool, count: int, workspace: Optional[torch.Tensor]):
+    """(the tensor, its address, its bytes)"""
     need = lib.qbn_kv_pool_workspace(pool._ref, count)
     if workspace is None:
-        return torch.empty(max(need, 0), dtype=torch.uint8, device=pool.device)
-    _need(workspace, need, "workspace")
-    _same_device(pool.table, (workspace, "workspace"))
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace
+        workspace = pool.table.new_empty(max(need, 0) // 4)
+        return workspace, workspace.data_ptr(), need
+    return (workspace,) + _given_workspace(workspace, need, pool.index)
 
 
 def _word(t: Optional[torch.Tensor], pool: KVPool, name: str) -> torch.Tensor:
     if t is None:
-        return torch.empty(1, dtype=torch.int32, device=pool.device)
-    _ints(t, 1, name)
-    _same_device(pool.table, (t, name))
+        return pool.table.new_empty(1)
+    _ints(t, 1, pool.index, name)
     return t
 
 
@@ -320,14 +363,13 @@ def kv_reserve(pool: KVPool, rows: torch.Tensor, tokens: torch.Tensor, out: Opti
     slots grow, the lowest free pages are taken in the order of the requests.
     Returns a device int32: -1, or the first request that cannot be met (then
     nothing changes). `out`: other tables to write, in place without."""
-    lib, out = _kv(), _pools(pool, out)
-    n = rows.numel()
-    _ints(rows, n, "rows")
-    _ints(tokens, n, "tokens")
-    _same_device(pool.table, (rows, "rows"), (tokens, "tokens"))
-    status, ws = _word(status, pool, "status"), _pool_workspace(lib, pool, n, workspace)
-    _check(lib.qbn_kv_reserve(pool._ref, out._ref, n, rows.data_ptr(), tokens.data_ptr(), status.data_ptr(),
-                              ws.data_ptr(), ws.numel() * ws.element_size(), _stream(pool.device)), "qbn_kv_reserve")
+    lib, out, dev, n = _bound or _kv(), _out(pool, out), pool.index, rows.numel()
+    r, t = _ints(rows, n, dev, "rows"), _ints(tokens, n, dev, "tokens")
+    status = _word(status, pool, "status")
+    workspace, ws, size = _pool_workspace(lib, pool, n, workspace)
+    st = lib.qbn_kv_reserve(pool._ref, out._ref, n, r, t, status.data_ptr(), ws, size, _raw_stream(dev))
+    if st:
+        raise QbnError(st, "qbn_kv_reserve")
     return status
 
 
@@ -337,15 +379,13 @@ def kv_fork(cache: KVCache, pool: KVPool, parents: torch.Tensor, children: torch
     """Slot children[i] (empty) becomes a copy of slot parents[i]: full pages are
     shared, a last page that is not full is copied in every layer. Returns the
     status word as kv_reserve does."""
-    lib, out = _kv(), _pools(pool, out, cache)
-    n = parents.numel()
-    _ints(parents, n, "parents")
-    _ints(children, n, "children")
-    _same_device(pool.table, (parents, "parents"), (children, "children"))
-    status, ws = _word(status, pool, "status"), _pool_workspace(lib, pool, n, workspace)
-    _check(lib.qbn_kv_fork(cache._ref, pool._ref, out._ref, n, parents.data_ptr(), children.data_ptr(),
-                           status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(pool.device)),
-           "qbn_kv_fork")
+    lib, out, dev, n = _bound or _kv(), _out(pool, out, cache), pool.index, parents.numel()
+    a, c = _ints(parents, n, dev, "parents"), _ints(children, n, dev, "children")
+    status = _word(status, pool, "status")
+    workspace, ws, size = _pool_workspace(lib, pool, n, workspace)
+    st = lib.qbn_kv_fork(cache._ref, pool._ref, out._ref, n, a, c, status.data_ptr(), ws, size, _raw_stream(dev))
+    if st:
+        raise QbnError(st, "qbn_kv_fork")
     return status
 
 
@@ -353,20 +393,20 @@ def kv_free(pool: KVPool, rows: torch.Tensor, window: int = 0, sinks: int = 0,
             out: Optional[KVPool] = None) -> None:
     """Give back the pages of slots rows[i]; with window > 0 only those that no
     later query of that window (and those sinks) sees, the slot going on."""
-    lib, out = _kv(), _pools(pool, out)
-    n = rows.numel()
-    _ints(rows, n, "rows")
-    _same_device(pool.table, (rows, "rows"))
-    _check(lib.qbn_kv_free(pool._ref, out._ref, n, rows.data_ptr(), window, sinks, _stream(pool.device)),
-           "qbn_kv_free")
+    lib, out, dev, n = _bound or _kv(), _out(pool, out), pool.index, rows.numel()
+    st = lib.qbn_kv_free(pool._ref, out._ref, n, _ints(rows, n, dev, "rows"), window, sinks, _raw_stream(dev))
+    if st:
+        raise QbnError(st, "qbn_kv_free")
 
 
 def kv_compact(cache: KVCache, pool: KVPool, out: Optional[KVPool] = None, live: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Pack the pool: the L pages in use end up in pages 0 .. L - 1 of every
     layer, the tables follow. Returns L as a device int32."""
-    lib, out = _kv(), _pools(pool, out, cache)
-    live, ws = _word(live, pool, "live"), _pool_workspace(lib, pool, 0, workspace)
-    _check(lib.qbn_kv_compact(cache._ref, pool._ref, out._ref, live.data_ptr(), ws.data_ptr(),
-                              ws.numel() * ws.element_size(), _stream(pool.device)), "qbn_kv_compact")
+    lib, out = _bound or _kv(), _out(pool, out, cache)
+    live = _word(live, pool, "live")
+    workspace, ws, size = _pool_workspace(lib, pool, 0, workspace)
+    st = lib.qbn_kv_compact(cache._ref, pool._ref, out._ref, live.data_ptr(), ws, size, _raw_stream(pool.index))
+    if st:
+        raise QbnError(st, "qbn_kv_compact")
     return live
