@@ -23,11 +23,15 @@
 // vote), so the usual tile needs no cross-lane maximum and no rescaling:
 // the weights then stay below 2^8 and binary32 sums hold them.
 //
-// Splitting. The tiles of all (sequence, head group) pairs form one list that
-// a fixed number of workgroups shares evenly, whatever the lengths; each
-// workgroup finds its piece from the lengths (one scan). A pair that lies in
-// one workgroup is written at once; the pieces of the others go through the
-// workspace and a second kernel joins them in order.
+// Splitting. A workgroup takes a piece of one (sequence, head group) pair. How
+// many units of 128 tokens a piece has follows from the lengths: so many that
+// about `blocks` pieces come out of all pairs, whatever the lengths. The
+// pieces of a pair are alike; each workgroup finds its own by a scan of the
+// lengths. A pair of one piece is written at once; the pieces of the others go
+// through the workspace and a second kernel joins them in order. (Pieces that
+// run over the end of a pair into the next one would be more even, but the
+// workgroups that hold an end then pass twice through the chain of length,
+// page table, first tile and output, and that chain is most of a short call.)
 #include "kv_device.h"
 #include "kv_launch.h"
 
@@ -45,7 +49,7 @@ struct DecodeArgs {
     int64_t qt, qh;
     __bf16 *out;
     float *lse;
-    float *parts;  // slots of [16][D] sums, then [16] maxima and [16] sums of weights
+    float *parts;  // pieces: [16][D] sums, then [16] maxima and [16] sums of weights
     float scale;   // times log2 e
     int group, tiles, rows;  // query heads per key-value head, 16-row tiles of them, pairs per sequence
     int window, sinks, blocks, dim;
@@ -69,9 +73,36 @@ __device__ __forceinline__ Span span_of(const DecodeArgs &a, int len) {
     return s;
 }
 
-__device__ __forceinline__ int64_t per_block(const DecodeArgs &a, int64_t total) {
-    const int64_t p = (total + a.blocks - 1) / a.blocks;
-    return p < 2 ? 2 : p;
+// Units and pieces of the sequences, 64 at a time: each wave scans the lengths
+// for itself, which costs a load and a few lane moves and no barrier.
+struct Chunk {
+    int n, upto, all;  // of this lane's sequence, up to and with it, of all 64
+};
+__device__ __forceinline__ Chunk scan_of(int n) {
+    Chunk c;
+    c.n = n;
+    c.upto = wave_scan(n);
+    c.all = __builtin_amdgcn_readlane(c.upto, 63);
+    return c;
+}
+__device__ __forceinline__ int units_of(const DecodeArgs &a, int s0) {
+    const int s = s0 + (threadIdx.x & 63);
+    return s < a.b.seqs ? span_of(a, a.b.lens[s]).n : 0;  // < 2^24
+}
+__device__ __forceinline__ uint32_t pieces_of(uint32_t n, uint32_t per) { return (n + per - 1) / per; }
+
+struct Plan {
+    int first;     // units of sequences 0 .. 63, one per lane
+    uint32_t per;  // units of a piece at most
+};
+__device__ __forceinline__ Plan plan_units(const DecodeArgs &a) {
+    Plan p;
+    p.first = units_of(a, 0);
+    int64_t total = scan_of(p.first).all;
+    for (int s = 64; s < a.b.seqs; s += 64) total += scan_of(units_of(a, s)).all;
+    const int64_t per = div_i64(total * a.rows + a.blocks - 1, a.blocks);
+    p.per = (uint32_t)(per < 1 ? 1 : per < (1 << 24) ? per : 1 << 24);
+    return p;
 }
 
 // A wave's 32 tokens as loaded: K rows, V rows and their scales.
@@ -101,21 +132,28 @@ struct Decoder {
 
     __device__ __forceinline__ bool sees(int t) const { return t < sp.len && (t >= sp.lo || t < a.sinks); }
 
-    // The page of tokens t .. t + 15 (t % 16 == 0): page 0 where none of them is seen.
-    __device__ __forceinline__ int64_t page_of(int t) {
-        const bool any = t < sp.len && (t + 15 >= sp.lo || t < a.sinks);
-        if (!any) return 0;
-        const int p = a.b.table[(int64_t)b * a.b.row_stride + (t >> a.c.page_shift)];
-        if ((uint32_t)p >= (uint32_t)a.c.pages) {
-            bad = true;
-            return 0;
+    // The pages of tokens t .. t + 15 and t + 16 .. t + 31 (t % 32 == 0): page 0
+    // where none of them is seen.
+    struct Pages {
+        int p[2];
+    };
+    __device__ __forceinline__ Pages pages_of(int t0) {
+        Pages r;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = t0 + 16 * i;
+            const bool any = t < sp.len && (t + 15 >= sp.lo || t < a.sinks);
+            const int p = table_entry(a.b, b, any ? t >> a.c.page_shift : 0);
+            const bool page = (uint32_t)p < (uint32_t)a.c.pages;
+            bad |= any && !page;
+            r.p[i] = any && page ? p : 0;
         }
-        return p;
+        return r;
     }
 
-    __device__ __forceinline__ void load(T &r, int t0) {
+    __device__ __forceinline__ void load(T &r, int t0, Pages pages) {
         const int ps = 1 << a.c.page_shift;
-        const int64_t p0 = page_of(t0), p1 = page_of(t0 + 16);
+        const int64_t p0 = pages.p[0], p1 = pages.p[1];
         // K: rows 4g' + i of the first product are tokens 8g' + i, of the second 8g' + 4 + i
         {
             const int t = 8 * (m / 4) + m % 4;  // < 16 for m < 8
@@ -252,227 +290,233 @@ struct Decoder {
 };
 
 template <int F, int D>
-__global__ __launch_bounds__(256) void k_decode(DecodeArgs a) {
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) {
     using T = Tile<F, D>;
     constexpr int LD = D + 4;  // padded row: 16 heads' writes of one element land in different banks
     __shared__ float s_acc[4][16][LD];
     __shared__ float s_ref[4][16], s_sum[4][16];
-    __shared__ int64_t s_scan[5];
-    __shared__ int64_t s_start[2];  // sequence, units before it
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    // ---- this workgroup's piece of the list of units
-    int b, r, off;
-    int64_t left;
+    // ---- this workgroup's piece
+    int b, r, piece = 0, pieces = 1;
     if (a.parts == nullptr) {  // one workgroup per pair
         b = blockIdx.x / a.rows;
         r = blockIdx.x % a.rows;
-        off = 0;
-        left = (int64_t)1 << 40;
     } else {
-        const int each = (a.b.seqs + 255) / 256;
-        int64_t mine = 0;
-        for (int i = 0; i < each; ++i) {
-            const int s = tid * each + i;
-            if (s < a.b.seqs) mine += span_of(a, a.b.lens[s]).n;
+        const Plan p = plan_units(a);
+        Chunk c = scan_of(pieces_of(p.first, p.per));
+        int64_t before = 0;
+        int s0 = 0;
+        while (blockIdx.x >= (before + c.all) * a.rows) {
+            before += c.all;
+            s0 += 64;
+            if (s0 >= a.b.seqs) return;  // more workgroups than pieces
+            c = scan_of(pieces_of(units_of(a, s0), p.per));
         }
-        int64_t total;
-        int64_t before = block_scan<256>(mine, s_scan, total);
-        const int64_t per = per_block(a, total * a.rows), start = blockIdx.x * per;
-        if (start >= total * a.rows) return;
-        if (before * a.rows <= start && start < (before + mine) * a.rows) {
-            for (int i = 0; i < each; ++i) {
-                const int s = tid * each + i;
-                const int n = span_of(a, a.b.lens[s]).n;
-                if (start < (before + n) * a.rows) {
-                    s_start[0] = s;
-                    s_start[1] = before;
-                    break;
-                }
-                before += n;
-            }
-        }
-        __syncthreads();
-        b = (int)s_start[0];
-        const int64_t rem = start - s_start[1] * a.rows;
-        const int n = span_of(a, a.b.lens[b]).n;
-        r = (int)(rem / n);
-        off = (int)(rem % n);
-        left = per;
+        const int at = __builtin_ctzll(__ballot(blockIdx.x < (before + c.upto) * a.rows));
+        b = s0 + at;
+        pieces = __builtin_amdgcn_readlane(c.n, at);
+        const uint32_t rest = (uint32_t)(blockIdx.x - (before + __builtin_amdgcn_readlane(c.upto, at) - pieces) * a.rows);
+        r = rest / pieces;
+        piece = rest % pieces;
     }
 
-    while (left > 0 && b < a.b.seqs) {
-        Decoder<F, D> w{a};
-        w.lane = lane;
-        w.m = lane & 15;
-        w.g = lane >> 4;
-        w.b = __builtin_amdgcn_readfirstlane(b);
-        w.kv_head = __builtin_amdgcn_readfirstlane(r / a.tiles);
-        w.sp = span_of(a, a.b.lens[w.b]);
-        const int n = w.sp.n, u1 = (int)(off + left < n ? off + left : n);
-        if (n > 0 || a.parts == nullptr) {
-            const int h0 = r % a.tiles * 16, heads = min(16, a.group - h0);
-            const int hq = w.kv_head * a.group + h0;  // first query head of the pair
-            // Q as the right operand, in the element order of K's pieces
-            bf16x8 q[D / 32];
+    Decoder<F, D> w{a};
+    w.lane = lane;
+    w.m = lane & 15;
+    w.g = lane >> 4;
+    w.b = __builtin_amdgcn_readfirstlane(b);
+    w.kv_head = __builtin_amdgcn_readfirstlane(r / a.tiles);
+    w.sp = span_of(a, length_of(a.b, w.b));
+    const int h0 = r % a.tiles * 16, heads = min(16, a.group - h0);
+    const int hq = w.kv_head * a.group + h0;  // first query head of the pair
+    const int u0 = (int)((int64_t)w.sp.n * piece / pieces), u1 = (int)((int64_t)w.sp.n * (piece + 1) / pieces);
+    // Q as the right operand, in the element order of K's pieces
+    bf16x8 q[D / 32];
 #pragma unroll
-            for (int s = 0; s < D / 32; ++s) {
-                const int d = (s * 8 / T::E * 4 + w.g) * T::E + s * 8 % T::E;
-                u32x4 t = {0, 0, 0, 0};
-                if (w.m < heads) t = ld16(a.q + (int64_t)w.b * a.qt + (int64_t)(hq + w.m) * a.qh + d);
-                q[s] = as_bf16x8(t);
-            }
-            f32x4 acc[D / 16];
+    for (int s = 0; s < D / 32; ++s) {
+        const int d = (s * 8 / T::E * 4 + w.g) * T::E + s * 8 % T::E;
+        u32x4 t = {0, 0, 0, 0};
+        if (w.m < heads) t = ld16(a.q + (int64_t)w.b * a.qt + (int64_t)(hq + w.m) * a.qh + d);
+        q[s] = as_bf16x8(t);
+    }
+    f32x4 acc[D / 16];
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) acc[t] = f32x4{0, 0, 0, 0};
-            float ref = kNegInf, sum = 0.0f;
-            T cur, nxt;
-            if (off < u1) w.load(cur, w.unit_token(off) + 32 * wave);
-            for (int u = off; u < u1; u += 2) {
-                if (u + 1 < u1) w.load(nxt, w.unit_token(u + 1) + 32 * wave);
-                w.step(cur, w.unit_token(u) + 32 * wave, q, ref, sum, acc);
-                if (u + 1 < u1) {
-                    if (u + 2 < u1) w.load(cur, w.unit_token(u + 2) + 32 * wave);
-                    w.step(nxt, w.unit_token(u + 1) + 32 * wave, q, ref, sum, acc);
-                }
-            }
-            // ---- the four waves' sums meet in LDS
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (w.bad || w.sp.bad) sum = __builtin_nanf("");
-            if (lane < 16) {
-                s_ref[wave][lane] = ref;
-                s_sum[wave][lane] = sum;
-            }
-            __syncthreads();
-            {
-                float top = s_ref[0][w.m];
-#pragma unroll
-                for (int i = 1; i < 4; ++i) top = __builtin_fmaxf(top, s_ref[i][w.m]);
-                const float f = ref == top ? 1.0f : exp2_fast(ref - top);
-#pragma unroll
-                for (int t = 0; t < D / 16; ++t) {
-                    constexpr int A8 = T::N8 * 8;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = 4 * w.g + i;
-                        const int d = t < A8 ? t / 8 * 128 + row * 8 + t % 8
-                                             : t < A8 + 4 * T::N4 ? T::N8 * 128 + row * 4 + (t - A8)
-                                                                  : T::N8 * 128 + T::N4 * 64 + row * 2 + (t - A8 - 4 * T::N4);
-                        s_acc[wave][w.m][d] = acc[t][i] * f;
-                    }
-                }
-            }
-            __syncthreads();
-            const bool all = off == 0 && u1 == n;
-            const int64_t slot = (int64_t)blockIdx.x + (int64_t)w.b * a.rows + r;
-            float *part = a.parts + slot * (16 * D + 32);
-            for (int i = tid; i < heads * (D / 4); i += 256) {
-                const int h = i / (D / 4), d = i % (D / 4) * 4;
-                float top = s_ref[0][h];
-#pragma unroll
-                for (int k = 1; k < 4; ++k) top = __builtin_fmaxf(top, s_ref[k][h]);
-                float total = 0.0f;
-                f32x4 o = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float rk = s_ref[k][h];
-                    total += s_sum[k][h] * (rk == top ? 1.0f : exp2_fast(rk - top));
-                    o += *reinterpret_cast<const f32x4 *>(&s_acc[k][h][d]);
-                }
-                if (all) {
-                    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-                    const int64_t row = (int64_t)w.b * a.rows / a.tiles * a.group + hq + h;
-                    *reinterpret_cast<u32x2 *>(a.out + row * D + d) =
-                        u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
-                    if (d == 0 && a.lse) a.lse[row] = total == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(total)) * kLn2;
-                } else {
-                    *reinterpret_cast<f32x4 *>(part + h * D + d) = o;
-                    if (d == 0) {
-                        part[16 * D + h] = top;
-                        part[16 * D + 16 + h] = total;
-                    }
-                }
-            }
-            __syncthreads();  // before the next pair overwrites LDS
+    for (int t = 0; t < D / 16; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    float ref = kNegInf, sum = 0.0f;
+    T cur, nxt;
+    const auto token = [&](int u) { return w.unit_token(u) + 32 * wave; };
+    // Two tiles in turn, the next one's loads in flight. The loop's loads are
+    // unconditional, so that the wait for one tile leaves the other's in
+    // flight: the last one or two units come after it.
+    if (u0 < u1) {
+        w.load(cur, token(u0), w.pages_of(token(u0)));
+        auto next = w.pages_of(token(u0 + 1));
+        int u = u0;
+        for (; u + 2 < u1; u += 2) {
+            w.load(nxt, token(u + 1), next);
+            next = w.pages_of(token(u + 2));
+            w.step(cur, token(u), q, ref, sum, acc);
+            w.load(cur, token(u + 2), next);
+            next = w.pages_of(token(u + 3));
+            w.step(nxt, token(u + 1), q, ref, sum, acc);
         }
-        if (a.parts == nullptr) return;
-        left -= u1 - off;
-        off = 0;
-        if (++r == a.rows) {
-            r = 0;
-            ++b;
+        if (u + 1 < u1) w.load(nxt, token(u + 1), next);
+        w.step(cur, token(u), q, ref, sum, acc);
+        if (u + 1 < u1) w.step(nxt, token(u + 1), q, ref, sum, acc);
+    }
+    // ---- the four waves' sums meet in LDS
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (w.bad || w.sp.bad) sum = __builtin_nanf("");
+    if (lane < 16) {
+        s_ref[wave][lane] = ref;
+        s_sum[wave][lane] = sum;
+    }
+    __syncthreads();
+    {
+        float top = s_ref[0][w.m];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) top = __builtin_fmaxf(top, s_ref[i][w.m]);
+        const float f = ref == top ? 1.0f : exp2_fast(ref - top);
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+            constexpr int A8 = T::N8 * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 4 * w.g + i;
+                const int d = t < A8 ? t / 8 * 128 + row * 8 + t % 8
+                                     : t < A8 + 4 * T::N4 ? T::N8 * 128 + row * 4 + (t - A8)
+                                                          : T::N8 * 128 + T::N4 * 64 + row * 2 + (t - A8 - 4 * T::N4);
+                s_acc[wave][w.m][d] = acc[t][i] * f;
+            }
+        }
+    }
+    __syncthreads();
+    float *part = a.parts + (int64_t)blockIdx.x * (16 * D + 32);
+    for (int i = tid; i < heads * (D / 4); i += 256) {
+        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        float top = s_ref[0][h];
+#pragma unroll
+        for (int k = 1; k < 4; ++k) top = __builtin_fmaxf(top, s_ref[k][h]);
+        float total = 0.0f;
+        f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float rk = s_ref[k][h];
+            total += s_sum[k][h] * (rk == top ? 1.0f : exp2_fast(rk - top));
+            o += *reinterpret_cast<const f32x4 *>(&s_acc[k][h][d]);
+        }
+        if (pieces == 1) {
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            const int64_t row = (int64_t)w.b * a.rows / a.tiles * a.group + hq + h;
+            *reinterpret_cast<u32x2 *>(a.out + row * D + d) =
+                u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+            if (d == 0 && a.lse) a.lse[row] = total == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(total)) * kLn2;
+        } else {
+            *reinterpret_cast<f32x4 *>(part + h * D + d) = o;
+            if (d == 0) {
+                part[16 * D + h] = top;
+                part[16 * D + 16 + h] = total;
+            }
         }
     }
 }
 
-// Joins the pieces of each pair, in order: a wave per (sequence, query head).
-template <int D>
+// Joins the pieces of each pair, in order. W waves per (sequence, query head):
+// one where there are many heads (few of them are split), four where there
+// are few (their pieces are many). D / 4 lanes take a piece, and all pieces
+// of the first round are loaded before their references are known.
+template <int D, int W>
 __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a) {
-    __shared__ int64_t s_scan[5];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int quads = (a.group + 3) / 4;  // workgroups per key-value head: four query heads each
-    const int kv_heads = a.rows / a.tiles;
-    const int b = blockIdx.x / (kv_heads * quads), rest = blockIdx.x % (kv_heads * quads);
-    const int kv_head = rest / quads, hg = rest % quads * 4 + wave;
-    // units before this sequence, and of all
-    int64_t mine = 0, all = 0;
-    for (int s = tid; s < a.b.seqs; s += 256) {
-        const int n = span_of(a, a.b.lens[s]).n;
-        all += n;
-        if (s < b) mine += n;
+    constexpr int L = D / 4, PW = 64 / L, SUBS = W * PW, SLOT = 16 * D + 32, R = 4;
+    __shared__ float s_o[4 * PW][D];
+    __shared__ float s_sum[4 * PW];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kv_heads = a.rows / a.tiles, q_heads = kv_heads * a.group;
+    const int64_t row = (int64_t)blockIdx.x * (4 / W) + wave / W;  // sequence, query head
+    if (row >= (int64_t)a.b.seqs * q_heads) return;                // W == 1 only: no barrier below
+    const int b = (int)(row / q_heads), hq = (int)(row % q_heads);
+    const int kv_head = hq / a.group, hg = hq % a.group;
+    // pieces before this sequence, and its own
+    const Plan p = plan_units(a);
+    int64_t before = 0;
+    Chunk c = scan_of(pieces_of(p.first, p.per));
+    for (int s = 64; s <= b; s += 64) {
+        before += c.all;
+        c = scan_of(pieces_of(units_of(a, s), p.per));
     }
-    int64_t total, before;
-    block_scan<256>(all, s_scan, total);
-    block_scan<256>(mine, s_scan, before);
-    const Span sp = span_of(a, a.b.lens[b]);
-    if (hg >= a.group) return;
-    const int64_t row = ((int64_t)b * kv_heads + kv_head) * a.group + hg;
-    if (sp.n == 0) {
-        const float none = sp.bad ? __builtin_nanf("") : 0.0f;
+    const int count = __builtin_amdgcn_readlane(c.n, b & 63);
+    before += __builtin_amdgcn_readlane(c.upto, b & 63) - count;
+    if (count == 0) {
+        const float none = span_of(a, length_of(a.b, b)).bad ? __builtin_nanf("") : 0.0f;
         for (int d = lane; d < D; d += 64) a.out[row * D + d] = (__bf16)none;
-        if (lane == 0 && a.lse) a.lse[row] = sp.bad ? none : kNegInf;
+        if (lane == 0 && a.lse) a.lse[row] = none == 0.0f ? kNegInf : none;
         return;
     }
-    const int64_t per = per_block(a, total * a.rows);
-    const int r = kv_head * a.tiles + hg / 16;
-    const int64_t u0 = before * a.rows + (int64_t)r * sp.n;
-    const int64_t i0 = u0 / per, i1 = (u0 + sp.n - 1) / per;
-    if (i0 == i1) return;  // written by its workgroup
-    const float *part = a.parts + (i0 + (int64_t)b * a.rows + r) * (16 * D + 32);
-    const int h = hg % 16, count = (int)(i1 - i0 + 1);
+    if (count == 1) return;  // written by its workgroup
+    const int r = kv_head * a.tiles + hg / 16, h = hg % 16;
+    const float *part = a.parts + (before * a.rows + (int64_t)r * count) * SLOT;
+    const int sub = wave % W * PW + lane / L, d = lane % L * 4;
+    const bool on = lane < PW * L;
+    const auto at = [&](int k) { return part + (int64_t)(k * SUBS + sub < count ? k * SUBS + sub : 0) * SLOT; };
+    f32x4 v[R];
+    float vr[R], vs[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        v[k] = *reinterpret_cast<const f32x4 *>(at(k) + h * D + d);
+        vr[k] = at(k)[16 * D + h];
+        vs[k] = at(k)[16 * D + 16 + h];
+    }
     float top = kNegInf;
-    for (int i = lane; i < count; i += 64) top = __builtin_fmaxf(top, part[(int64_t)i * (16 * D + 32) + 16 * D + h]);
+    for (int i = lane; i < count; i += 64) top = __builtin_fmaxf(top, part[(int64_t)i * SLOT + 16 * D + h]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    constexpr int PER = (D + 63) / 64;
-    float o[PER] = {}, sum = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-        const float *p = part + (int64_t)i * (16 * D + 32);
-        const float ri = p[16 * D + h];
-        const float f = ri == top ? 1.0f : exp2_fast(ri - top);
-        sum += f * p[16 * D + 16 + h];
+    for (int k = 1; k < 64; k <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, k));
+    f32x4 o = {0, 0, 0, 0};
+    float sum = 0.0f;
+    const auto add = [&](int k, f32x4 x, float ref, float s) {
+        if (k * SUBS + sub < count) {
+            const float f = ref == top ? 1.0f : exp2_fast(ref - top);
+            o += x * f;
+            sum += s * f;
+        }
+    };
 #pragma unroll
-        for (int e = 0; e < PER; ++e)
-            if (D % 64 == 0 || e * 64 + lane < D) o[e] += f * p[h * D + e * 64 + lane];
+    for (int k = 0; k < R; ++k) add(k, v[k], vr[k], vs[k]);
+    for (int k = R; k * SUBS < count; ++k) {
+        const float *p = at(k);
+        add(k, *reinterpret_cast<const f32x4 *>(p + h * D + d), p[16 * D + h], p[16 * D + 16 + h]);
+    }
+    // the W waves' parts meet in LDS
+    const int s0 = wave / W * SUBS;
+    if (on) {
+        *reinterpret_cast<f32x4 *>(&s_o[s0 + sub][d]) = o;
+        if (d == 0) s_sum[s0 + sub] = sum;
+    }
+    if constexpr (W > 1) __syncthreads();
+    else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
+    if (wave % W != 0 || lane >= L) return;
+    o = f32x4{0, 0, 0, 0};
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < SUBS; ++k) {
+        o += *reinterpret_cast<const f32x4 *>(&s_o[s0 + k][d]);
+        sum += s_sum[s0 + k];
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < PER; ++e)
-        if (D % 64 == 0 || e * 64 + lane < D) a.out[row * D + e * 64 + lane] = (__bf16)(o[e] * inv);
+    *reinterpret_cast<u32x2 *>(a.out + row * D + d) = u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
     if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // How the host cuts the work: the most units a sequence can have (from the
 // table's width, the window and the sinks), and the number of workgroups.
-struct Plan {
+struct Cut {
     int64_t units, pairs, blocks;
     int tiles;
 };
 
-Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
-    Plan p;
+Cut plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
+    Cut p;
     p.tiles = (q_heads / c.heads + 15) / 16;
     p.pairs = b.seqs * c.heads * p.tiles;
     p.units = (b.row * c.page_size + kUnit - 1) / kUnit;
@@ -480,19 +524,27 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
         const int64_t seen = (int64_t)window / kUnit + 2 + ((int64_t)sinks + kUnit - 1) / kUnit;
         if (seen < p.units) p.units = seen;
     }
-    // Up to two units a pair: one workgroup each. More: 1024 workgroups, four
-    // per compute unit, share the units.
-    p.blocks = p.units <= 2 ? 0 : p.pairs * p.units / 2 < 1024 ? p.pairs * p.units / 2 + 1 : 1024;
+    p.blocks = p.units <= 2 ? 0 : 512;
     return p;
 }
 
+// Pieces at most: a pair of n units has less than n / per + 1, with per at
+// least total / blocks; and none has less than one unit.
+int64_t most_pieces(const Cut &p) {
+    const int64_t most = p.blocks + p.pairs;
+    return p.pairs * p.units < most ? p.pairs * p.units : most;
+}
+
 template <int F>
-hipError_t launch(const DecodeArgs &a, int64_t grid, int64_t join, hipStream_t s) {
-    const dim3 g((unsigned)grid), gj((unsigned)join);
+hipError_t launch(const DecodeArgs &a, int64_t grid, hipStream_t s) {
+    const dim3 g((unsigned)grid);
+    const int64_t rows = (int64_t)a.b.seqs * a.rows / a.tiles * a.group;
 #define QBN_KV_DIM(DD)                                            \
     case DD:                                                      \
         k_decode<F, DD><<<g, 256, 0, s>>>(a);                     \
-        if (a.parts) k_decode_join<DD><<<gj, 256, 0, s>>>(a);     \
+        if (!a.parts) break;                                      \
+        if (rows < 1024) k_decode_join<DD, 4><<<(unsigned)rows, 256, 0, s>>>(a);              \
+        else k_decode_join<DD, 1><<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(a);              \
         break;
     switch (a.dim) {
         QBN_KV_DIM(64)
@@ -508,13 +560,13 @@ hipError_t launch(const DecodeArgs &a, int64_t grid, int64_t join, hipStream_t s
 }  // namespace
 
 int64_t kv_decode_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
-    const Plan p = plan_of(c, b, q_heads, window, sinks);
-    return p.blocks ? (p.blocks + p.pairs) * (16 * (int64_t)c.head_dim + 32) * 4 : 0;
+    const Cut p = plan_of(c, b, q_heads, window, sinks);
+    return p.blocks ? most_pieces(p) * (16 * (int64_t)c.head_dim + 32) * 4 : 0;
 }
 
 hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, int q_heads, const KvRows &q,
                             float scale, int window, int sinks, void *out, float *lse, void *ws, hipStream_t s) {
-    const Plan p = plan_of(c, b, q_heads, window, sinks);
+    const Cut p = plan_of(c, b, q_heads, window, sinks);
     const int64_t elems = layer * c.pages * c.heads * c.page_size * c.head_dim;
     const int bits = c.format == QBN_KV_BF16 ? 16 : c.format == QBN_MXFP8 ? 8 : 4;
     DecodeArgs a;
@@ -529,10 +581,9 @@ hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_b
     a.scale = scale * kLog2e;
     a.group = q_heads / c.heads, a.tiles = p.tiles, a.rows = c.heads * p.tiles;
     a.window = window, a.sinks = sinks, a.blocks = (int)p.blocks, a.dim = c.head_dim;
-    const int64_t grid = p.blocks ? p.blocks : p.pairs;
-    const int64_t join = b.seqs * c.heads * ((a.group + 3) / 4);
-    if (c.format == QBN_KV_BF16) return launch<BF16>(a, grid, join, s);
-    return c.format == QBN_MXFP8 ? launch<FP8>(a, grid, join, s) : launch<FP4>(a, grid, join, s);
+    const int64_t grid = p.blocks ? most_pieces(p) : p.pairs;
+    if (c.format == QBN_KV_BF16) return launch<BF16>(a, grid, s);
+    return c.format == QBN_MXFP8 ? launch<FP8>(a, grid, s) : launch<FP4>(a, grid, s);
 }
 
 }  // namespace qbn

@@ -33,6 +33,19 @@ __device__ __forceinline__ float e8m0_f32(uint32_t b) {
     return __builtin_amdgcn_ldexpf(1.0f, e8m0_exponent(b));
 }
 
+// Entry `i` of sequence b's table row, both the same in the whole wave. A scalar
+// load: it waits on its own counter, so that looking up the next pages does
+// not wait for the loads of K and V that are in flight (vector loads return
+// in order). No kernel that calls this writes the table.
+__device__ __forceinline__ int table_entry(const Batch &b, int seq, int i) {
+    typedef const int32_t __attribute__((address_space(4))) *Const;
+    return ((Const)(uintptr_t)b.table)[(int64_t)seq * b.row_stride + i];
+}
+__device__ __forceinline__ int length_of(const Batch &b, int seq) {
+    typedef const int32_t __attribute__((address_space(4))) *Const;
+    return ((Const)(uintptr_t)b.lens)[seq];
+}
+
 // Eight consecutive elements (4, 8 or 16 bytes in w) -> bf16 pairs, exact: an
 // E2M1 or E4M3FN value has at most 4 significant bits.
 template <int F>
@@ -116,6 +129,28 @@ __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast
 // 2^-126 may come out as 0; a softmax term that small is 2^-126 of the row's
 // largest.
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int dpp_i32(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+
+// Inclusive sums over the lanes of a wave: shifts within rows of 16, then the
+// last lane of row 0 (2) to row 1 (3) and of row 1 to rows 2 and 3.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp_i32<0x111>(v);
+    v += dpp_i32<0x112>(v);
+    v += dpp_i32<0x114>(v);
+    v += dpp_i32<0x118>(v);
+    v += dpp_i32<0x142, 0xA>(v);
+    v += dpp_i32<0x143, 0xC>(v);
+    return v;
+}
+
+// a / b for a >= 0, b > 0, the same in all lanes: the 64-bit division is 130 instructions long.
+__device__ __forceinline__ int64_t div_i64(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // Sums over the threads of a workgroup of NT threads; every thread gets the
 // sum of all threads and the sum of those before it. `lds` holds NT / 64 + 1

@@ -157,20 +157,19 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 
     uint32_t raw[L::ITEMS][L::RAW];
     u32x2 rsc[L::ITEMS];
-    const auto load = [&](int t0) {
-        int page[4];
+    int page[4];  // of the tile to be loaded next
+    const auto look_up = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = t0 + 16 * i;
             const bool any = t <= pmax && (t + 15 >= lo || t < a.sinks);
-            int p = 0;
-            if (any) p = a.b.table[(int64_t)b * a.b.row_stride + (t >> a.c.page_shift)];
-            if ((uint32_t)p >= (uint32_t)a.c.pages) {
-                bad = true;
-                p = 0;
-            }
-            page[i] = p;
+            const int p = table_entry(a.b, b, any ? t >> a.c.page_shift : 0);
+            const bool ok = (uint32_t)p < (uint32_t)a.c.pages;
+            bad |= any && !ok;
+            page[i] = any && ok ? p : 0;
         }
+    };
+    const auto load = [&](int t0) {
         const auto base_of = [&](int t) {
             const int i = t >> 4;
             const int p = i < 2 ? (i == 0 ? page[0] : page[1]) : (i == 2 ? page[2] : page[3]);
@@ -318,13 +317,16 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     if (tid == 0) s_odd = 0;
     __syncthreads();
     if (u0 < u1) {
+        look_up(tile_token(u0));
         load(tile_token(u0));
+        if (u0 + 1 < u1) look_up(tile_token(u0 + 1));
         store(tile_token(u0), 0);
     }
     __syncthreads();
     for (int u = u0; u < u1; ++u) {
         const int buf = (u - u0) & 1;
         if (u + 1 < u1) load(tile_token(u + 1));
+        if (u + 2 < u1) look_up(tile_token(u + 2));
         compute(tile_token(u), buf);
         if (u + 1 < u1) store(tile_token(u + 1), buf ^ 1);
         __syncthreads();
