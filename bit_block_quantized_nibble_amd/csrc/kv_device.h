@@ -111,6 +111,15 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
     }
 }
 
+// Four 16-bit elements of a column from LDS: the 16 lanes of a row of lanes
+// address 8 bytes each, four lanes a matrix row of 16 elements, and lane i gets
+// column i of the four rows.
+__device__ __forceinline__ u32x2 ld_tr16(const uint8_t *lds) {
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s *Lds;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)lds));
+}
+
 // The words of eight tokens (row j: W elements as bf16 pairs) -> for each
 // element t, the eight tokens' values as four dwords: the A operand of a
 // matrix product over tokens.

@@ -5,15 +5,17 @@
 // heads that share K and V share the loads and the expansion to bf16, and a
 // chunk of a few tokens still fills rows. K and V go through LDS in tiles of
 // 64 tokens, two buffers, the next tile's bytes in registers while this one
-// is computed; K as [token][head_dim] with 16 bytes of padding, V transposed
-// ([head_dim][token], 16-byte pieces swizzled), so that both operands of both
-// products are 16-byte LDS reads without bank conflicts.
+// is computed. Both lie there as [token][head_dim], rows padded by 16 (K) and
+// 32 bytes (V): K's matrix operand is 16 bytes of a row, V's is read column
+// by column with the transposing LDS load, four tokens at a time.
 //
-// As in the decode kernel the products are transposed: S^T = K Q^T with the
-// rows of K permuted so that a lane's scores are exactly the eight tokens per
-// step that it supplies to out^T = V^T P^T. A lane owns one row: the softmax
-// needs no cross-lane work but one exchange between the two halves of a wave,
-// and only when a score exceeds the running reference by 2^8.
+// The products are transposed: S^T = K Q^T leaves with each lane, for one row,
+// the scores of tokens 4h .. 4h + 3 of every eight (h: the lane's half of the
+// wave), and those are the tokens for which it then supplies the softmax
+// weights as the right operand of out^T = V^T P^T; V's columns are read in
+// the same order. A lane owns one row: the softmax needs no cross-lane work
+// but one exchange between the two halves of a wave, and only when a score
+// exceeds the running reference by 2^8.
 //
 // Bound by the matrix cores together with the exponentials and LDS reads.
 #include "kv_device.h"
@@ -34,24 +36,24 @@ struct PrefillArgs {
     __bf16 *out;
     float *lse;
     float *parts;  // [splits][tokens][heads][D] sums, then [splits][tokens][heads] references and weight sums
-    float scale;   // times log2 e
+    float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
+    uint32_t q_keep, q_flip;
     int group, window, sinks, splits, dim;
 };
 
 template <int F, int D, int NW>
 struct Lay {
     static constexpr int NT = NW * 64, BM = NW * 32;
-    static constexpr int KROW = 2 * D + 16;         // bytes of a K row in LDS
+    // Bytes of a row in LDS: an odd number of 16-byte pieces, so that eight
+    // rows' same piece lie in all banks, and an even number that is 2 (mod 8)
+    // or 6, so that four rows' 32 bytes do.
+    static constexpr int KROW = 2 * D + 16, VROW = 2 * D + 32;
     static constexpr int VOFF = BN * KROW;
-    static constexpr int BUF = VOFF + D * 2 * BN;   // one buffer
-    static constexpr int HALF = 2 * D;              // K items (32 elements of a token); as many V items (4 x 8 tokens)
-    static constexpr int ITEMS = (2 * HALF + NT - 1) / NT;
-    static constexpr int KW = kBits<F>;             // words of a K item
-    static constexpr int VW = F == BF16 ? 2 : 1;    // words of a V item's token
-    static constexpr int RAW = (KW > 8 * VW ? KW : 8 * VW);
+    static constexpr int BUF = VOFF + BN * VROW;  // one buffer
+    static constexpr int PER = D / 16;            // items (16 elements of a token's K and V) of a row
+    static constexpr int ALL = BN * PER, ITEMS = (ALL + NT - 1) / NT;
+    static constexpr int IB = 2 * kBits<F>, IW = IB / 4;  // bytes and words of an item
 };
-
-__device__ __forceinline__ int v_swizzle(int d) { return ((d >> 1) ^ (d >> 4)) & 7; }
 
 // A sequence's new tokens, as far as cu is in order and inside q.
 __device__ __forceinline__ int new_tokens(const Batch &b, int s, int &first) {
@@ -81,6 +83,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     using L = Lay<F, D, NW>;
     __shared__ __align__(16) uint8_t s_buf[2][L::BUF];
     __shared__ int s_odd;  // a tile that not every row sees held an infinity or NaN of V
+    __shared__ int s_bad;  // a visible token's table entry was no page
     __shared__ int64_t s_scan[NW + 1];
     __shared__ int s_at[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -120,7 +123,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     const int r0 = tile * L::BM;
     int len = a.b.lens[b];
     const int ps = 1 << a.c.page_shift;
-    bool bad = len < 0 || (((int64_t)len + ps - 1) >> a.c.page_shift) > a.b.row;
+    const bool bad = len < 0 || (((int64_t)len + ps - 1) >> a.c.page_shift) > a.b.row;
     if (bad) len = 0;
     // this lane's row; rows beyond the last repeat it and are not written
     const int r = r0 + wave * 32 + n;
@@ -139,7 +142,12 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     {
         const __bf16 *row = a.q + (int64_t)(q0 + qi) * a.qt + (int64_t)head * a.qh + 8 * half;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) q[k] = as_bf16x8(ld16(row + 16 * k));
+        for (int k = 0; k < D / 16; ++k) {
+            u32x4 t = ld16(row + 16 * k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = (t[i] & a.q_keep) ^ a.q_flip;
+            q[k] = as_bf16x8(t);
+        }
     }
     f32x16 acc[D / 32];
 #pragma unroll
@@ -155,122 +163,109 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     };
     const auto is_seen = [&](int t) { return t <= pmax && (t >= lo || t < a.sinks); };
 
-    uint32_t raw[L::ITEMS][L::RAW];
-    u32x2 rsc[L::ITEMS];
-    int page[4];  // of the tile to be loaded next
+    // ---- a thread's part of a tile: its items' page table entries, bytes and scales
+    const int32_t *row_table = a.b.table + (int64_t)b * a.b.row_stride;
+    int entry[L::ITEMS];
+    uint32_t raw_k[L::ITEMS][L::IW], raw_v[L::ITEMS][L::IW];
+    uint32_t sc_k[L::ITEMS], sc_v[L::ITEMS];
+    const auto item = [&](int i, int &t, int &blk) {
+        const int it = tid + i * L::NT;
+        t = it / L::PER, blk = it % L::PER;
+        return L::ALL % L::NT == 0 || it < L::ALL;
+    };
     const auto look_up = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 16 * i;
-            const bool any = t <= pmax && (t + 15 >= lo || t < a.sinks);
-            const int p = table_entry(a.b, b, any ? t >> a.c.page_shift : 0);
-            const bool ok = (uint32_t)p < (uint32_t)a.c.pages;
-            bad |= any && !ok;
-            page[i] = any && ok ? p : 0;
+        for (int i = 0; i < L::ITEMS; ++i) {
+            int t, blk;
+            entry[i] = 0;
+            if (item(i, t, blk) && is_seen(t0 + t)) entry[i] = row_table[(t0 + t) >> a.c.page_shift];
         }
     };
     const auto load = [&](int t0) {
-        const auto base_of = [&](int t) {
-            const int i = t >> 4;
-            const int p = i < 2 ? (i == 0 ? page[0] : page[1]) : (i == 2 ? page[2] : page[3]);
-            return (int64_t)p * a.c.heads + kv_head;
-        };
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
-            const int it = tid + i * L::NT;
-            if (it < L::HALF) {
-                const int t = it / (D / 32), blk = it % (D / 32), slot = (t0 + t) & (ps - 1);
-                const int64_t h = base_of(t);
-                load_words<4 * L::KW>(a.c.k + ((h * ps + slot) * D + blk * 32) * kBits<F> / 8, raw[i]);
-                if constexpr (F != BF16) rsc[i].x = a.c.ks[(h * (D / 32) + blk) * ps + slot];
-            } else if (it < 2 * L::HALF) {
-                const int v = it - L::HALF, tg = v / (D / 4), dg = v % (D / 4), slot = (t0 + 8 * tg) & (ps - 1);
-                const int64_t h = base_of(8 * tg);
-                const uint8_t *p = a.c.v + ((h * ps + slot) * D + dg * 4) * kBits<F> / 8;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) load_words<kBits<F> / 2>(p + j * (D * kBits<F> / 8), raw[i] + j * L::VW);
-                if constexpr (F != BF16) rsc[i] = ld8(a.c.vs + (h * (D / 32) + dg / 8) * ps + slot);
+            int t, blk;
+            if (!item(i, t, blk)) continue;
+            uint32_t p = entry[i];
+            if (p >= (uint32_t)a.c.pages) {
+                s_bad = 1;
+                p = 0;
+            }
+            const int64_t rows0 = (int64_t)((uint64_t)p * (uint32_t)(a.c.heads << a.c.page_shift)) + (kv_head << a.c.page_shift);
+            const int slot = (t0 + t) & (ps - 1);
+            const int64_t o = (rows0 + slot) * (D * kBits<F> / 8) + blk * L::IB;
+            load_words<L::IB>(a.c.k + o, raw_k[i]);
+            load_words<L::IB>(a.c.v + o, raw_v[i]);
+            if constexpr (F != BF16) {
+                const int64_t so = rows0 * (D / 32) + ((blk / 2) << a.c.page_shift) + slot;
+                sc_k[i] = a.c.ks[so];
+                sc_v[i] = a.c.vs[so];
             }
         }
     };
     const auto store = [&](int t0, int buf) {
         const bool edge = is_edge(t0);
-        uint8_t *ks = s_buf[buf], *vs = s_buf[buf] + L::VOFF;
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
-            const int it = tid + i * L::NT;
-            if (it < L::HALF) {
-                const int t = it / (D / 32), blk = it % (D / 32);
-                const float sc = F == BF16 ? 1.0f : e8m0_f32(rsc[i].x);
+            int t, blk;
+            if (!item(i, t, blk)) continue;
+            const float fk = F == BF16 ? 1.0f : e8m0_f32(sc_k[i]), fv = F == BF16 ? 1.0f : e8m0_f32(sc_v[i]);
+            uint32_t k[2][4], v[2][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t o[4];
-                    expand8<F>(raw[i] + e * (L::KW / 4), sc, o);
-                    *reinterpret_cast<u32x4 *>(ks + t * L::KROW + blk * 64 + e * 16) = u32x4{o[0], o[1], o[2], o[3]};
-                }
-            } else if (it < 2 * L::HALF) {
-                const int v = it - L::HALF, tg = v / (D / 4), dg = v % (D / 4);
-                uint32_t c[8][2];
+            for (int e = 0; e < 2; ++e) {
+                expand8<F>(raw_k[i] + e * (L::IW / 2), fk, k[e]);
+                expand8<F>(raw_v[i] + e * (L::IW / 2), fv, v[e]);
+            }
+            if (edge) {  // what no row sees becomes 0; what only some see is looked over
+                const bool on = is_seen(t0 + t);
+                bool odd = false;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float sc = F == BF16 ? 1.0f : e8m0_f32((j < 4 ? rsc[i].x : rsc[i].y) >> (8 * (j & 3)));
-                    expand<F, 4>(raw[i] + j * L::VW, sc, c[j]);
-                }
-                if (edge) {  // what no row sees becomes 0; what only some see is looked over
-                    bool odd = false;
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bool on = is_seen(t0 + 8 * tg + j);
+                    for (int j = 0; j < 4; ++j) {
+                        v[e][j] = on ? v[e][j] : 0u;
+                        odd |= (v[e][j] & 0x7F80u) == 0x7F80u || (v[e][j] & 0x7F800000u) == 0x7F800000u;
+                    }
+                if (__any(odd)) {  // taken out of the product; put where they belong at the end
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            c[j][k] = on ? c[j][k] : 0u;
-                            odd |= (c[j][k] & 0x7F80u) == 0x7F80u || (c[j][k] & 0x7F800000u) == 0x7F800000u;
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            v[e][j] &= (v[e][j] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
+                            v[e][j] &= (v[e][j] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : 0xFFFFFFFFu;
                         }
-                    }
-                    if (__any(odd)) {  // taken out of the product; add_special puts them where they belong
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                c[j][k] &= (c[j][k] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
-                                c[j][k] &= (c[j][k] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : 0xFFFFFFFFu;
-                            }
-                        s_odd = 1;
-                    }
+                    s_odd = 1;
                 }
+            }
+            uint8_t *kd = s_buf[buf] + t * L::KROW + blk * 32, *vd = s_buf[buf] + L::VOFF + t * L::VROW + blk * 32;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = dg * 4 + e;
-                    *reinterpret_cast<u32x4 *>(vs + d * (2 * BN) + ((tg ^ v_swizzle(d)) * 16)) = column8<4>(c, e);
-                }
+            for (int e = 0; e < 2; ++e) {
+                *reinterpret_cast<u32x4 *>(kd + 16 * e) = u32x4{k[e][0], k[e][1], k[e][2], k[e][3]};
+                *reinterpret_cast<u32x4 *>(vd + 16 * e) = u32x4{v[e][0], v[e][1], v[e][2], v[e][3]};
             }
         }
     };
 
-    const int krow = 16 * (n / 16) + 8 * (n / 4 % 2) + 4 * (n / 8 % 2) + n % 4;  // the token of this lane's K row
+    const int koff = n * L::KROW + 16 * half;
+    const int voff = L::VOFF + (4 * half + (lane & 15) / 4) * L::VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
     const auto compute = [&](int t0, int buf) {
-        const uint8_t *ks = s_buf[buf], *vs = s_buf[buf] + L::VOFF;
+        const uint8_t *ks = s_buf[buf] + koff, *vs = s_buf[buf] + voff;
         f32x16 s[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    as_bf16x8(ld16(ks + (t * 32 + krow) * L::KROW + (16 * k + 8 * half) * 2)), q[k], s[t], 0, 0, 0);
-        }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[t][e] *= a.scale;
-        const bool edge = is_edge(t0);
-        if (edge) {
+            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(ld16(ks + t * 32 * L::KROW + 32 * k)), q[k], s[t], 0, 0, 0);
+        if (is_edge(t0)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const int k = t0 + 32 * t + 16 * (e / 8) + 8 * half + e % 8;
+                    const int k = t0 + 32 * t + 8 * (e / 4) + 4 * half + e % 4;
                     const bool on = k <= pos && (a.window == 0 || k > pos - a.window || k < a.sinks);
                     s[t][e] = on ? s[t][e] : kNegInf;
                 }
@@ -280,6 +275,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[t][e]);
+        top *= a.scale;
         if (__any(top > ref + 8.0f)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
             const float now = __builtin_fmaxf(ref, top);
@@ -292,29 +288,29 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         const float base = ref == kNegInf ? 0.0f : ref;
         bf16x8 p[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int g = 0; g < 4; ++g) {
+            u32x4 w;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                u32x4 w;
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float x = exp2_fast(s[t][8 * g + j] - base), y = exp2_fast(s[t][8 * g + j + 1] - base);
-                    sum += x + y;
-                    w[j / 2] = pack_bf16x2(x, y);
-                }
-                p[2 * t + g] = as_bf16x8(w);
+            for (int j = 0; j < 8; j += 2) {
+                const int e = 8 * (g & 1) + j;
+                const float x = exp2_fast(__builtin_fmaf(s[g / 2][e], a.scale, -base));
+                const float y = exp2_fast(__builtin_fmaf(s[g / 2][e + 1], a.scale, -base));
+                sum += x + y;
+                w[j / 2] = pack_bf16x2(x, y);
             }
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t) {
-            const int d = 32 * t + n;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    as_bf16x8(ld16(vs + d * (2 * BN) + (((2 * i + half) ^ v_swizzle(d)) * 16))), p[i], acc[t], 0, 0, 0);
+            p[g] = as_bf16x8(w);
         }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t) {
+                const uint8_t *v = vs + 16 * g * L::VROW + 64 * t;
+                const u32x2 lo = ld_tr16(v), hi = ld_tr16(v + 8 * L::VROW);
+                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(u32x4{lo.x, lo.y, hi.x, hi.y}), p[g], acc[t], 0, 0, 0);
+            }
     };
 
-    if (tid == 0) s_odd = 0;
+    if (tid == 0) s_odd = s_bad = 0;
     __syncthreads();
     if (u0 < u1) {
         look_up(tile_token(u0));
@@ -333,7 +329,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     }
 
     sum += __shfl_xor(sum, 32);
-    if (bad) sum = __builtin_nanf("");
+    if (bad || s_bad) sum = __builtin_nanf("");
     const int64_t total = (int64_t)a.b.tokens * (a.c.heads * a.group), shift = total * blockIdx.y;
     const int64_t row = (int64_t)(q0 + qi) * (a.c.heads * a.group) + head;
     if (mine && a.splits == 1) {
@@ -477,7 +473,9 @@ hipError_t launch_kv_prefill(const qbn_kv_cache &c, int64_t layer, const qbn_kv_
     a.qt = q.token_stride, a.qh = q.head_stride;
     a.out = (__bf16 *)out, a.lse = lse;
     a.parts = (float *)ws;
-    a.scale = scale * kLog2e;
+    a.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
+    a.q_keep = scale == 0.0f ? 0u : ~0u;
+    a.q_flip = scale < 0.0f ? 0x80008000u : 0u;
     a.group = q_heads / c.heads, a.window = window, a.sinks = sinks, a.splits = p.splits, a.dim = c.head_dim;
     const dim3 grid((unsigned)(p.tiles * c.heads), (unsigned)p.splits);
     if (c.format == QBN_KV_BF16) return launch<BF16>(a, grid, s);
