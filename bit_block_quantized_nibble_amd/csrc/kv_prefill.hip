@@ -169,23 +169,25 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     uint32_t raw_k[L::ITEMS][L::IW], raw_v[L::ITEMS][L::IW];
     uint32_t sc_k[L::ITEMS], sc_v[L::ITEMS];
     const auto item = [&](int i, int &t, int &blk) {
-        const int it = tid + i * L::NT;
+        int it = tid + i * L::NT;
+        if (L::ALL % L::NT) it = min(it, L::ALL - 1);  // threads without an item repeat the last
         t = it / L::PER, blk = it % L::PER;
-        return L::ALL % L::NT == 0 || it < L::ALL;
     };
+    // Unconditional loads, here and in load: behind a branch the compiler
+    // could not tell which are in flight, and would wait for all of them.
     const auto look_up = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
             int t, blk;
-            entry[i] = 0;
-            if (item(i, t, blk) && is_seen(t0 + t)) entry[i] = row_table[(t0 + t) >> a.c.page_shift];
+            item(i, t, blk);
+            entry[i] = row_table[(is_seen(t0 + t) ? t0 + t : pmax) >> a.c.page_shift];  // pmax is seen
         }
     };
     const auto load = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
             int t, blk;
-            if (!item(i, t, blk)) continue;
+            item(i, t, blk);
             uint32_t p = entry[i];
             if (p >= (uint32_t)a.c.pages) {
                 s_bad = 1;
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
             int t, blk;
-            if (!item(i, t, blk)) continue;
+            item(i, t, blk);
             const float fk = F == BF16 ? 1.0f : e8m0_f32(sc_k[i]), fv = F == BF16 ? 1.0f : e8m0_f32(sc_v[i]);
             uint32_t k[2][4], v[2][4];
 #pragma unroll
@@ -315,17 +317,18 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     if (u0 < u1) {
         look_up(tile_token(u0));
         load(tile_token(u0));
-        if (u0 + 1 < u1) look_up(tile_token(u0 + 1));
+        look_up(tile_token(u0 + 1));
         store(tile_token(u0), 0);
-    }
-    __syncthreads();
-    for (int u = u0; u < u1; ++u) {
-        const int buf = (u - u0) & 1;
-        if (u + 1 < u1) load(tile_token(u + 1));
-        if (u + 2 < u1) look_up(tile_token(u + 2));
-        compute(tile_token(u), buf);
-        if (u + 1 < u1) store(tile_token(u + 1), buf ^ 1);
         __syncthreads();
+        for (int u = u0; u + 1 < u1; ++u) {
+            const int buf = (u - u0) & 1;
+            load(tile_token(u + 1));
+            look_up(tile_token(u + 2));
+            compute(tile_token(u), buf);
+            store(tile_token(u + 1), buf ^ 1);
+            __syncthreads();
+        }
+        compute(tile_token(u1 - 1), (u1 - 1 - u0) & 1);
     }
 
     sum += __shfl_xor(sum, 32);
