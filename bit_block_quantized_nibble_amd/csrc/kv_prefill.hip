@@ -44,16 +44,22 @@ struct PrefillArgs {
 template <int F, int D, int NW>
 struct Lay {
     static constexpr int NT = NW * 64, BM = NW * 32;
-    // Bytes of a row in LDS: an odd number of 16-byte pieces, so that eight
-    // rows' same piece lie in all banks, and an even number that is 2 (mod 8)
-    // or 6, so that four rows' 32 bytes do.
-    static constexpr int KROW = 2 * D + 16, VROW = 2 * D + 32;
-    static constexpr int VOFF = BN * KROW;
-    static constexpr int BUF = VOFF + BN * VROW;  // one buffer
+    // Bytes of a row in LDS (64 banks, 16 pieces of 16 bytes): an odd number of
+    // pieces, so that sixteen rows' same piece lie in all banks, and 4 or 12
+    // pieces (mod 16), so that four rows' 64 bytes do.
+    static constexpr int KROW = 2 * D + 16, VROW = 2 * D + (D == 96 ? 0 : 64);
+    static constexpr int KBUF = BN * KROW, VBUF = BN * VROW;  // one buffer each
     static constexpr int PER = D / 16;            // items (16 elements of a token's K and V) of a row
     static constexpr int ALL = BN * PER, ITEMS = (ALL + NT - 1) / NT;
     static constexpr int IB = 2 * kBits<F>, IW = IB / 4;  // bytes and words of an item
 };
+
+// The value, computed where this stands: the optimizer may not move it to its use.
+template <typename T>
+__device__ __forceinline__ T here(T v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 // A sequence's new tokens, as far as cu is in order and inside q.
 __device__ __forceinline__ int new_tokens(const Batch &b, int s, int &first) {
@@ -81,7 +87,7 @@ __device__ __forceinline__ float element(const Cache &c, int64_t head, int ps, i
 template <int F, int D, int NW>
 __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a) {
     using L = Lay<F, D, NW>;
-    __shared__ __align__(16) uint8_t s_buf[2][L::BUF];
+    __shared__ __align__(16) uint8_t s_k[2][L::KBUF], s_v[2][L::VBUF];
     __shared__ int s_odd;  // a tile that not every row sees held an infinity or NaN of V
     __shared__ int s_bad;  // a visible token's table entry was no page
     __shared__ int64_t s_scan[NW + 1];
@@ -165,16 +171,15 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 
     // ---- a thread's part of a tile: its items' page table entries, bytes and scales
     const int32_t *row_table = a.b.table + (int64_t)b * a.b.row_stride;
-    int entry[L::ITEMS];
-    uint32_t raw_k[L::ITEMS][L::IW], raw_v[L::ITEMS][L::IW];
-    uint32_t sc_k[L::ITEMS], sc_v[L::ITEMS];
     const auto item = [&](int i, int &t, int &blk) {
         int it = tid + i * L::NT;
         if (L::ALL % L::NT) it = min(it, L::ALL - 1);  // threads without an item repeat the last
         t = it / L::PER, blk = it % L::PER;
     };
-    // Unconditional loads, here and in load: behind a branch the compiler
-    // could not tell which are in flight, and would wait for all of them.
+    uint32_t raw[L::ITEMS][L::IW], sc[L::ITEMS];  // K's or V's, in turn
+    uint32_t entry[L::ITEMS], entry_v[L::ITEMS];
+    // Unconditional loads, here and below: behind a branch the compiler could
+    // not tell which are in flight, and would wait for all of them.
     const auto look_up = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
@@ -183,41 +188,49 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             entry[i] = row_table[(is_seen(t0 + t) ? t0 + t : pmax) >> a.c.page_shift];  // pmax is seen
         }
     };
-    const auto load = [&](int t0) {
+    const auto load = [&](const uint8_t *elements, const uint8_t *scales, int t0, const uint32_t (&pages)[L::ITEMS]) {
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
             int t, blk;
             item(i, t, blk);
-            uint32_t p = entry[i];
+            uint32_t p = pages[i];
             if (p >= (uint32_t)a.c.pages) {
                 s_bad = 1;
                 p = 0;
             }
             const int64_t rows0 = (int64_t)((uint64_t)p * (uint32_t)(a.c.heads << a.c.page_shift)) + (kv_head << a.c.page_shift);
             const int slot = (t0 + t) & (ps - 1);
-            const int64_t o = (rows0 + slot) * (D * kBits<F> / 8) + blk * L::IB;
-            load_words<L::IB>(a.c.k + o, raw_k[i]);
-            load_words<L::IB>(a.c.v + o, raw_v[i]);
-            if constexpr (F != BF16) {
-                const int64_t so = rows0 * (D / 32) + ((blk / 2) << a.c.page_shift) + slot;
-                sc_k[i] = a.c.ks[so];
-                sc_v[i] = a.c.vs[so];
-            }
+            load_words<L::IB>(elements + (rows0 + slot) * (D * kBits<F> / 8) + blk * L::IB, raw[i]);
+            if constexpr (F != BF16) sc[i] = scales[rows0 * (D / 32) + ((blk / 2) << a.c.page_shift) + slot];
         }
     };
-    const auto store = [&](int t0, int buf) {
+    const auto expand_item = [&](int i, uint32_t (&x)[2][4]) {
+        const float f = F == BF16 ? 1.0f : e8m0_f32(sc[i]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) expand8<F>(raw[i] + e * (L::IW / 2), f, x[e]);
+    };
+    const auto put = [&](uint8_t *d, const uint32_t (&x)[2][4]) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) *reinterpret_cast<u32x4 *>(d + 16 * e) = u32x4{x[e][0], x[e][1], x[e][2], x[e][3]};
+    };
+    const auto store_k = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < L::ITEMS; ++i) {
+            int t, blk;
+            item(i, t, blk);
+            uint32_t x[2][4];
+            expand_item(i, x);
+            put(s_k[buf] + t * L::KROW + blk * 32, x);
+        }
+    };
+    const auto store_v = [&](int t0, int buf) {
         const bool edge = is_edge(t0);
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
             int t, blk;
             item(i, t, blk);
-            const float fk = F == BF16 ? 1.0f : e8m0_f32(sc_k[i]), fv = F == BF16 ? 1.0f : e8m0_f32(sc_v[i]);
-            uint32_t k[2][4], v[2][4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                expand8<F>(raw_k[i] + e * (L::IW / 2), fk, k[e]);
-                expand8<F>(raw_v[i] + e * (L::IW / 2), fv, v[e]);
-            }
+            uint32_t x[2][4];
+            expand_item(i, x);
             if (edge) {  // what no row sees becomes 0; what only some see is looked over
                 const bool on = is_seen(t0 + t);
                 bool odd = false;
@@ -225,43 +238,61 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        v[e][j] = on ? v[e][j] : 0u;
-                        odd |= (v[e][j] & 0x7F80u) == 0x7F80u || (v[e][j] & 0x7F800000u) == 0x7F800000u;
+                        x[e][j] = on ? x[e][j] : 0u;
+                        odd |= (x[e][j] & 0x7F80u) == 0x7F80u || (x[e][j] & 0x7F800000u) == 0x7F800000u;
                     }
                 if (__any(odd)) {  // taken out of the product; put where they belong at the end
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            v[e][j] &= (v[e][j] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
-                            v[e][j] &= (v[e][j] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : 0xFFFFFFFFu;
+                            x[e][j] &= (x[e][j] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
+                            x[e][j] &= (x[e][j] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : 0xFFFFFFFFu;
                         }
                     s_odd = 1;
                 }
             }
-            uint8_t *kd = s_buf[buf] + t * L::KROW + blk * 32, *vd = s_buf[buf] + L::VOFF + t * L::VROW + blk * 32;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                *reinterpret_cast<u32x4 *>(kd + 16 * e) = u32x4{k[e][0], k[e][1], k[e][2], k[e][3]};
-                *reinterpret_cast<u32x4 *>(vd + 16 * e) = u32x4{v[e][0], v[e][1], v[e][2], v[e][3]};
-            }
+            put(s_v[buf] + t * L::VROW + blk * 32, x);
         }
     };
 
-    const int koff = n * L::KROW + 16 * half;
-    const int voff = L::VOFF + (4 * half + (lane & 15) / 4) * L::VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-    const auto compute = [&](int t0, int buf) {
-        const uint8_t *ks = s_buf[buf] + koff, *vs = s_buf[buf] + voff;
+    struct Scores {
         f32x16 s[2];
+    };
+    const int koff = n * L::KROW + 16 * half;
+    const int voff = (4 * half + (lane & 15) / 4) * L::VROW + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+    // Matrix operands, read from LDS in the order of the products' steps.
+    constexpr int SK = D / 8, SV = D / 8, AHEAD = 4;
+    const auto k_part = [&](int buf, int i) { return as_bf16x8(ld16(s_k[buf] + koff + i % 2 * 32 * L::KROW + 32 * (i / 2))); };
+    const auto v_part = [&](int buf, int i) {
+        const uint8_t *v = s_v[buf] + voff + 16 * (i / (D / 32)) * L::VROW + 64 * (i % (D / 32));
+        const u32x2 lo = ld_tr16(v), hi = ld_tr16(v + 8 * L::VROW);
+        return as_bf16x8(u32x4{lo.x, lo.y, hi.x, hi.y});
+    };
+    const auto scores = [&](Scores &x, int buf) {
+#pragma unroll
+        for (int i = 0; i < SK; ++i) {
+            if (i < 2) x.s[i] = f32x16{};
+            x.s[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_part(buf, i), q[i / 2], x.s[i % 2], 0, 0, 0);
+        }
+    };
+    // Word w of the weights: scores 2w and 2w + 1.
+    const auto weight = [&](const Scores &x, float base, int w) {
+        const float y = exp2_fast(__builtin_fmaf(x.s[w / 8][2 * w % 16], a.scale, -base));
+        const float z = exp2_fast(__builtin_fmaf(x.s[w / 8][2 * w % 16 + 1], a.scale, -base));
+        sum += y + z;
+        return pack_bf16x2(y, z);
+    };
+    const auto largest = [&](const Scores &x) {
+        float top = x.s[0][0];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(ld16(ks + t * 32 * L::KROW + 32 * k)), q[k], s[t], 0, 0, 0);
+            for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, x.s[t][e]);
+        return top;
+    };
+    // Masks the scores of an edge and raises the reference where they exceed it.
+    const auto settle = [&](Scores &x, float top, int t0) {
         if (is_edge(t0)) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -269,14 +300,10 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
                 for (int e = 0; e < 16; ++e) {
                     const int k = t0 + 32 * t + 8 * (e / 4) + 4 * half + e % 4;
                     const bool on = k <= pos && (a.window == 0 || k > pos - a.window || k < a.sinks);
-                    s[t][e] = on ? s[t][e] : kNegInf;
+                    x.s[t][e] = on ? x.s[t][e] : kNegInf;
                 }
+            top = largest(x);
         }
-        float top = s[0][0];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[t][e]);
         top *= a.scale;
         if (__any(top > ref + 8.0f)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
@@ -287,48 +314,95 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 #pragma unroll
             for (int t = 0; t < D / 32; ++t) acc[t] *= f;
         }
-        const float base = ref == kNegInf ? 0.0f : ref;
-        bf16x8 p[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            u32x4 w;
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const int e = 8 * (g & 1) + j;
-                const float x = exp2_fast(__builtin_fmaf(s[g / 2][e], a.scale, -base));
-                const float y = exp2_fast(__builtin_fmaf(s[g / 2][e + 1], a.scale, -base));
-                sum += x + y;
-                w[j / 2] = pack_bf16x2(x, y);
-            }
-            p[g] = as_bf16x8(w);
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int t = 0; t < D / 32; ++t) {
-                const uint8_t *v = vs + 16 * g * L::VROW + 64 * t;
-                const u32x2 lo = ld_tr16(v), hi = ld_tr16(v + 8 * L::VROW);
-                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(u32x4{lo.x, lo.y, hi.x, hi.y}), p[g], acc[t], 0, 0, 0);
-            }
     };
-
     if (tid == 0) s_odd = s_bad = 0;
     __syncthreads();
+    // K runs a tile ahead of V: the scores of the next tile are computed next to
+    // the exponentials of this one.
     if (u0 < u1) {
+        const auto move_on = [&](int t0) {
+#pragma unroll
+            for (int i = 0; i < L::ITEMS; ++i) entry_v[i] = entry[i];
+            look_up(t0);
+        };
         look_up(tile_token(u0));
-        load(tile_token(u0));
+        load(a.c.k, a.c.ks, tile_token(u0), entry);
+        store_k(0);
+        load(a.c.v, a.c.vs, tile_token(u0), entry);
         look_up(tile_token(u0 + 1));
-        store(tile_token(u0), 0);
+        store_v(tile_token(u0), 0);
+        load(a.c.k, a.c.ks, tile_token(u0 + 1), entry);
+        move_on(tile_token(u0 + 2));
+        store_k(1);
         __syncthreads();
-        for (int u = u0; u + 1 < u1; ++u) {
+        Scores s0, s1;
+        scores(s0, 0);
+        settle(s0, largest(s0), tile_token(u0));
+        __syncthreads();  // the first turn overwrites the first K
+        // One tile: its scores are in x, the next one's go to y. The order of the
+        // steps is kept by the scheduling barriers: next to each matrix product
+        // of K stand a pair's exponentials, next to V's a piece of the maximum,
+        // and the operands are read AHEAD steps before their use.
+        const auto turn = [&](int u, Scores &x, Scores &y) {
             const int buf = (u - u0) & 1;
-            load(tile_token(u + 1));
-            look_up(tile_token(u + 2));
-            compute(tile_token(u), buf);
-            store(tile_token(u + 1), buf ^ 1);
+            load(a.c.v, a.c.vs, tile_token(u + 1), entry_v);
+            const float base = ref == kNegInf ? 0.0f : ref;
+            u32x4 p[4];
+            bf16x8 part[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) part[i] = k_part(buf ^ 1, i);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < SK; ++i) {
+                if (i < 2) y.s[i] = f32x16{};
+                y.s[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part[i % AHEAD], q[i / 2], y.s[i % 2], 0, 0, 0);
+                part[i % AHEAD] = i + AHEAD < SK ? k_part(buf ^ 1, i + AHEAD) : v_part(buf, i + AHEAD - SK);
+#pragma unroll
+                for (int w = 16 * i / SK; w < 16 * (i + 1) / SK; ++w) p[w / 4][w % 4] = here(weight(x, base, w));
+                sum = here(sum);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            store_v(tile_token(u + 1), buf ^ 1);
+            load(a.c.k, a.c.ks, tile_token(u + 2), entry);
+            move_on(tile_token(u + 3));
+            __builtin_amdgcn_sched_barrier(0);
+            float top = y.s[0][0];
+#pragma unroll
+            for (int i = 0; i < SV; ++i) {
+                const int t = i % (D / 32), g = i / (D / 32);
+                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part[i % AHEAD], as_bf16x8(p[g]), acc[t], 0, 0, 0);
+                if (i + AHEAD < SV) part[i % AHEAD] = v_part(buf, i + AHEAD);
+#pragma unroll
+                for (int w = 16 * i / SV; w < 16 * (i + 1) / SV; ++w)
+                    top = here(__builtin_fmaxf(top, __builtin_fmaxf(y.s[w / 8][2 * w % 16], y.s[w / 8][2 * w % 16 + 1])));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            store_k(buf);
+            settle(y, top, tile_token(u + 1));
             __syncthreads();
+        };
+        const auto last = [&](int u, Scores &x) {
+            const int buf = (u - u0) & 1;
+            const float base = ref == kNegInf ? 0.0f : ref;
+            u32x4 p[4];
+#pragma unroll
+            for (int w = 0; w < 16; ++w) p[w / 4][w % 4] = weight(x, base, w);
+#pragma unroll
+            for (int i = 0; i < SV; ++i)
+                acc[i % (D / 32)] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_part(buf, i), as_bf16x8(p[i / (D / 32)]),
+                                                                            acc[i % (D / 32)], 0, 0, 0);
+        };
+        int u = u0;
+        for (; u + 2 < u1; u += 2) {
+            turn(u, s0, s1);
+            turn(u + 1, s1, s0);
         }
-        compute(tile_token(u1 - 1), (u1 - 1 - u0) & 1);
+        if (u + 1 < u1) {
+            turn(u, s0, s1);
+            last(u + 1, s1);
+        } else {
+            last(u, s0);
+        }
     }
 
     sum += __shfl_xor(sum, 32);
