@@ -26,8 +26,8 @@ int32_t check_shape(int32_t format, int64_t layers, int64_t pages, int32_t heads
     if (!known_page(page_size)) return QBN_ERR_SHAPE;
     if (!known_dim(head_dim)) return QBN_ERR_UNSUPPORTED;
     if (layers <= 0 || pages <= 0 || heads <= 0) return QBN_ERR_SHAPE;
-    if (pages > kMaxTokens || heads > (1 << 16) || layers > (1 << 20)) return QBN_ERR_SHAPE;
-    const int64_t page = (int64_t)heads * page_size * head_dim;  // < 2^32
+    if (pages > kMaxTokens || heads > (1 << 12) || layers > (1 << 20)) return QBN_ERR_SHAPE;
+    const int64_t page = (int64_t)heads * page_size * head_dim;  // < 2^28, so that a page's bytes fit 32 bits
     if (pages > kMaxElems / page || layers > kMaxElems / (page * pages)) return QBN_ERR_SHAPE;
     *elems = layers * pages * page;
     return QBN_OK;

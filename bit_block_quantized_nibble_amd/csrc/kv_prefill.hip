@@ -162,12 +162,14 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
     float ref = kNegInf, sum = 0.0f;
 
+    // Conditions without short circuits: as branches they cost more than they save.
     const auto tile_token = [&](int u) { return (u < sink_tiles ? u : u - sink_tiles + first) * BN; };
+    const auto token_after = [&](int t0) { return t0 + BN == sink_tiles * BN ? first * BN : t0 + BN; };
     // tokens that every row of the workgroup sees need no mask
     const auto is_edge = [&](int t0) {
-        return t0 + BN - 1 > pmin || (a.window > 0 && t0 <= pmax - a.window && t0 + BN > a.sinks);
+        return (int)(t0 + BN - 1 > pmin) | ((int)(a.window > 0) & (int)(t0 <= pmax - a.window) & (int)(t0 + BN > a.sinks));
     };
-    const auto is_seen = [&](int t) { return t <= pmax && (t >= lo || t < a.sinks); };
+    const auto is_seen = [&](int t) { return (t <= pmax) & ((t >= lo) | (t < a.sinks)); };
 
     // ---- a thread's part of a tile: its items' page table entries, bytes and scales
     const int32_t *row_table = a.b.table + (int64_t)b * a.b.row_stride;
@@ -178,31 +180,34 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     };
     uint32_t raw[L::ITEMS][L::IW], sc[L::ITEMS];  // K's or V's, in turn
     uint32_t entry[L::ITEMS], entry_v[L::ITEMS];
+    constexpr int ROW = D * kBits<F> / 8;  // bytes
+    const uint32_t page_rows = (uint32_t)a.c.heads << a.c.page_shift;
+    const int64_t head_rows = (int64_t)kv_head << a.c.page_shift;
+    const uint8_t *k_head = a.c.k + head_rows * ROW, *v_head = a.c.v + head_rows * ROW;
+    const uint8_t *ks_head = a.c.ks + head_rows * (D / 32), *vs_head = a.c.vs + head_rows * (D / 32);
     // Unconditional loads, here and below: behind a branch the compiler could
-    // not tell which are in flight, and would wait for all of them.
-    const auto look_up = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < L::ITEMS; ++i) {
-            int t, blk;
-            item(i, t, blk);
-            entry[i] = row_table[(is_seen(t0 + t) ? t0 + t : pmax) >> a.c.page_shift];  // pmax is seen
-        }
+    // not tell which are in flight, and would wait for all of them. Tokens
+    // beyond the last visible one stand for that one.
+    const auto look_up = [&](int i, int t0) {
+        int t, blk;
+        item(i, t, blk);
+        const uint32_t at = (uint32_t)min(t0 + t, pmax) >> a.c.page_shift;
+        entry[i] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(row_table) + at * 4);
     };
-    const auto load = [&](const uint8_t *elements, const uint8_t *scales, int t0, const uint32_t (&pages)[L::ITEMS]) {
-#pragma unroll
-        for (int i = 0; i < L::ITEMS; ++i) {
-            int t, blk;
-            item(i, t, blk);
-            uint32_t p = pages[i];
-            if (p >= (uint32_t)a.c.pages) {
-                s_bad = 1;
-                p = 0;
+    const auto load = [&](int i, const uint8_t *elements, const uint8_t *scales, int t0, const uint32_t *pages) {
+        int t, blk;
+        item(i, t, blk);
+        uint32_t page = pages[i];
+        if (__any(page >= (uint32_t)a.c.pages)) {
+            if (page >= (uint32_t)a.c.pages) {
+                if (is_seen(t0 + t)) s_bad = 1;
+                page = 0;
             }
-            const int64_t rows0 = (int64_t)((uint64_t)p * (uint32_t)(a.c.heads << a.c.page_shift)) + (kv_head << a.c.page_shift);
-            const int slot = (t0 + t) & (ps - 1);
-            load_words<L::IB>(elements + (rows0 + slot) * (D * kBits<F> / 8) + blk * L::IB, raw[i]);
-            if constexpr (F != BF16) sc[i] = scales[rows0 * (D / 32) + ((blk / 2) << a.c.page_shift) + slot];
         }
+        const uint32_t slot = (uint32_t)(t0 + t) & (uint32_t)(ps - 1);
+        load_words<L::IB>(elements + blk * L::IB + slot * ROW + (uint64_t)page * (page_rows * ROW), raw[i]);
+        if constexpr (F != BF16)
+            sc[i] = scales[((blk / 2) << a.c.page_shift) + slot + (uint64_t)page * (page_rows * (D / 32))];
     };
     const auto expand_item = [&](int i, uint32_t (&x)[2][4]) {
         const float f = F == BF16 ? 1.0f : e8m0_f32(sc[i]);
@@ -223,8 +228,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             put(s_k[buf] + t * L::KROW + blk * 32, x);
         }
     };
-    const auto store_v = [&](int t0, int buf) {
-        const bool edge = is_edge(t0);
+    const auto store_v = [&](int t0, bool edge, int buf) {
 #pragma unroll
         for (int i = 0; i < L::ITEMS; ++i) {
             int t, blk;
@@ -292,8 +296,8 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         return top;
     };
     // Masks the scores of an edge and raises the reference where they exceed it.
-    const auto settle = [&](Scores &x, float top, int t0) {
-        if (is_edge(t0)) {
+    const auto settle = [&](Scores &x, float top, int t0, bool edge) {
+        if (edge) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -320,32 +324,45 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     // K runs a tile ahead of V: the scores of the next tile are computed next to
     // the exponentials of this one.
     if (u0 < u1) {
+        const auto load_k = [&](int t0) {
+#pragma unroll
+            for (int i = 0; i < L::ITEMS; ++i) load(i, k_head, ks_head, t0, entry);
+        };
         const auto move_on = [&](int t0) {
 #pragma unroll
-            for (int i = 0; i < L::ITEMS; ++i) entry_v[i] = entry[i];
-            look_up(t0);
+            for (int i = 0; i < L::ITEMS; ++i) {
+                entry_v[i] = entry[i];
+                look_up(i, t0);
+            }
         };
-        look_up(tile_token(u0));
-        load(a.c.k, a.c.ks, tile_token(u0), entry);
+        const auto load_v = [&](int t0) {
+#pragma unroll
+            for (int i = 0; i < L::ITEMS; ++i) load(i, v_head, vs_head, t0, entry_v);
+        };
+        const int t0 = tile_token(u0);
+        int t1 = token_after(t0), t2 = token_after(t1);  // of the next two tiles
+        move_on(t0);
+        load_k(t0);
         store_k(0);
-        load(a.c.v, a.c.vs, tile_token(u0), entry);
-        look_up(tile_token(u0 + 1));
-        store_v(tile_token(u0), 0);
-        load(a.c.k, a.c.ks, tile_token(u0 + 1), entry);
-        move_on(tile_token(u0 + 2));
+        move_on(t1);
+        load_v(t0);
+        store_v(t0, is_edge(t0), 0);
+        load_k(t1);
+        move_on(t2);
         store_k(1);
         __syncthreads();
         Scores s0, s1;
         scores(s0, 0);
-        settle(s0, largest(s0), tile_token(u0));
+        settle(s0, largest(s0), t0, is_edge(t0));
         __syncthreads();  // the first turn overwrites the first K
         // One tile: its scores are in x, the next one's go to y. The order of the
         // steps is kept by the scheduling barriers: next to each matrix product
         // of K stand a pair's exponentials, next to V's a piece of the maximum,
         // and the operands are read AHEAD steps before their use.
-        const auto turn = [&](int u, Scores &x, Scores &y) {
-            const int buf = (u - u0) & 1;
-            load(a.c.v, a.c.vs, tile_token(u + 1), entry_v);
+        const auto turn = [&](int buf, Scores &x, Scores &y) {
+            load_v(t1);
+            const int t3 = token_after(t2);
+            const bool edge = is_edge(t1);
             const float base = ref == kNegInf ? 0.0f : ref;
             u32x4 p[4];
             bf16x8 part[AHEAD];
@@ -362,9 +379,9 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
                 sum = here(sum);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            store_v(tile_token(u + 1), buf ^ 1);
-            load(a.c.k, a.c.ks, tile_token(u + 2), entry);
-            move_on(tile_token(u + 3));
+            store_v(t1, edge, buf ^ 1);
+            load_k(t2);
+            move_on(t3);
             __builtin_amdgcn_sched_barrier(0);
             float top = y.s[0][0];
 #pragma unroll
@@ -378,11 +395,11 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
                 __builtin_amdgcn_sched_barrier(0);
             }
             store_k(buf);
-            settle(y, top, tile_token(u + 1));
+            settle(y, top, t1, edge);
+            t1 = t2, t2 = t3;
             __syncthreads();
         };
-        const auto last = [&](int u, Scores &x) {
-            const int buf = (u - u0) & 1;
+        const auto last = [&](int buf, Scores &x) {
             const float base = ref == kNegInf ? 0.0f : ref;
             u32x4 p[4];
 #pragma unroll
@@ -394,14 +411,14 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         };
         int u = u0;
         for (; u + 2 < u1; u += 2) {
-            turn(u, s0, s1);
-            turn(u + 1, s1, s0);
+            turn(0, s0, s1);
+            turn(1, s1, s0);
         }
         if (u + 1 < u1) {
-            turn(u, s0, s1);
-            last(u + 1, s1);
+            turn(0, s0, s1);
+            last(1, s1);
         } else {
-            last(u, s0);
+            last(0, s0);
         }
     }
 
