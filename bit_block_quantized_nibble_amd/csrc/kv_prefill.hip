@@ -41,9 +41,9 @@ struct PrefillArgs {
     int group, window, sinks, splits, dim;
 };
 
-template <int F, int D, int NW>
+template <int F, int D>
 struct Lay {
-    static constexpr int NT = NW * 64, BM = NW * 32;
+    static constexpr int NW = 4, NT = NW * 64, BM = NW * 32;
     // Bytes of a row in LDS (64 banks, 16 pieces of 16 bytes): an odd number of
     // pieces, so that sixteen rows' same piece lie in all banks, and 4 or 12
     // pieces (mod 16), so that four rows' 64 bytes do.
@@ -84,13 +84,13 @@ __device__ __forceinline__ float element(const Cache &c, int64_t head, int ps, i
     return __uint_as_float(o[0] << 16);
 }
 
-template <int F, int D, int NW>
-__global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a) {
-    using L = Lay<F, D, NW>;
+template <int F, int D>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a) {
+    using L = Lay<F, D>;
     __shared__ __align__(16) uint8_t s_k[2][L::KBUF], s_v[2][L::VBUF];
     __shared__ int s_odd;  // a tile that not every row sees held an infinity or NaN of V
     __shared__ int s_bad;  // a visible token's table entry was no page
-    __shared__ int64_t s_scan[NW + 1];
+    __shared__ int64_t s_scan[L::NW + 1];
     __shared__ int s_at[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, half = lane >> 5;
@@ -157,9 +157,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     }
     f32x16 acc[D / 32];
 #pragma unroll
-    for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
+    for (int t = 0; t < D / 32; ++t) acc[t] = f32x16{};
     float ref = kNegInf, sum = 0.0f;
 
     // Conditions without short circuits: as branches they cost more than they save.
@@ -178,8 +176,13 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         if (L::ALL % L::NT) it = min(it, L::ALL - 1);  // threads without an item repeat the last
         t = it / L::PER, blk = it % L::PER;
     };
-    uint32_t raw[L::ITEMS][L::IW], sc[L::ITEMS];  // K's or V's, in turn
-    uint32_t entry[L::ITEMS], entry_v[L::ITEMS];
+    struct Items {
+        uint32_t w[L::ITEMS][L::IW], sc[L::ITEMS];
+    };
+    struct Entries {
+        uint32_t page[L::ITEMS];
+    };
+    Items rk, rv;
     constexpr int ROW = D * kBits<F> / 8;  // bytes
     const uint32_t page_rows = (uint32_t)a.c.heads << a.c.page_shift;
     const int64_t head_rows = (int64_t)kv_head << a.c.page_shift;
@@ -188,16 +191,16 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     // Unconditional loads, here and below: behind a branch the compiler could
     // not tell which are in flight, and would wait for all of them. Tokens
     // beyond the last visible one stand for that one.
-    const auto look_up = [&](int i, int t0) {
+    const auto look_up = [&](int i, int t0, Entries &e) {
         int t, blk;
         item(i, t, blk);
         const uint32_t at = (uint32_t)min(t0 + t, pmax) >> a.c.page_shift;
-        entry[i] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(row_table) + at * 4);
+        e.page[i] = *reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(row_table) + at * 4);
     };
-    const auto load = [&](int i, const uint8_t *elements, const uint8_t *scales, int t0, const uint32_t *pages) {
+    const auto load = [&](int i, const uint8_t *elements, const uint8_t *scales, int t0, const Entries &from, Items &r) {
         int t, blk;
         item(i, t, blk);
-        uint32_t page = pages[i];
+        uint32_t page = from.page[i];
         if (__any(page >= (uint32_t)a.c.pages)) {
             if (page >= (uint32_t)a.c.pages) {
                 if (is_seen(t0 + t)) s_bad = 1;
@@ -205,59 +208,53 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             }
         }
         const uint32_t slot = (uint32_t)(t0 + t) & (uint32_t)(ps - 1);
-        load_words<L::IB>(elements + blk * L::IB + slot * ROW + (uint64_t)page * (page_rows * ROW), raw[i]);
+        load_words<L::IB>(elements + blk * L::IB + slot * ROW + (uint64_t)page * (page_rows * ROW), r.w[i]);
         if constexpr (F != BF16)
-            sc[i] = scales[((blk / 2) << a.c.page_shift) + slot + (uint64_t)page * (page_rows * (D / 32))];
+            r.sc[i] = scales[((blk / 2) << a.c.page_shift) + slot + (uint64_t)page * (page_rows * (D / 32))];
     };
-    const auto expand_item = [&](int i, uint32_t (&x)[2][4]) {
-        const float f = F == BF16 ? 1.0f : e8m0_f32(sc[i]);
+    const auto expand_item = [&](const Items &r, int i, uint32_t (&x)[2][4]) {
+        const float f = F == BF16 ? 1.0f : e8m0_f32(r.sc[i]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) expand8<F>(raw[i] + e * (L::IW / 2), f, x[e]);
+        for (int e = 0; e < 2; ++e) expand8<F>(r.w[i] + e * (L::IW / 2), f, x[e]);
     };
     const auto put = [&](uint8_t *d, const uint32_t (&x)[2][4]) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) *reinterpret_cast<u32x4 *>(d + 16 * e) = u32x4{x[e][0], x[e][1], x[e][2], x[e][3]};
     };
-    const auto store_k = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < L::ITEMS; ++i) {
-            int t, blk;
-            item(i, t, blk);
-            uint32_t x[2][4];
-            expand_item(i, x);
-            put(s_k[buf] + t * L::KROW + blk * 32, x);
-        }
+    const auto store_k = [&](int i, int buf) {
+        int t, blk;
+        item(i, t, blk);
+        uint32_t x[2][4];
+        expand_item(rk, i, x);
+        put(s_k[buf] + t * L::KROW + blk * 32, x);
     };
-    const auto store_v = [&](int t0, bool edge, int buf) {
+    const auto store_v = [&](int i, int t0, bool edge, int buf) {
+        int t, blk;
+        item(i, t, blk);
+        uint32_t x[2][4];
+        expand_item(rv, i, x);
+        if (edge) {  // what no row sees becomes 0; what only some see is looked over
+            const bool on = is_seen(t0 + t);
+            bool odd = false;
 #pragma unroll
-        for (int i = 0; i < L::ITEMS; ++i) {
-            int t, blk;
-            item(i, t, blk);
-            uint32_t x[2][4];
-            expand_item(i, x);
-            if (edge) {  // what no row sees becomes 0; what only some see is looked over
-                const bool on = is_seen(t0 + t);
-                bool odd = false;
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[e][j] = on ? x[e][j] : 0u;
+                    odd |= (x[e][j] & 0x7F80u) == 0x7F80u || (x[e][j] & 0x7F800000u) == 0x7F800000u;
+                }
+            if (__any(odd)) {  // taken out of the product; put where they belong at the end
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        x[e][j] = on ? x[e][j] : 0u;
-                        odd |= (x[e][j] & 0x7F80u) == 0x7F80u || (x[e][j] & 0x7F800000u) == 0x7F800000u;
+                        x[e][j] &= (x[e][j] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
+                        x[e][j] &= (x[e][j] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : 0xFFFFFFFFu;
                     }
-                if (__any(odd)) {  // taken out of the product; put where they belong at the end
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            x[e][j] &= (x[e][j] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
-                            x[e][j] &= (x[e][j] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : 0xFFFFFFFFu;
-                        }
-                    s_odd = 1;
-                }
+                s_odd = 1;
             }
-            put(s_v[buf] + t * L::VROW + blk * 32, x);
         }
+        put(s_v[buf] + t * L::VROW + blk * 32, x);
     };
 
     struct Scores {
@@ -273,40 +270,40 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         const u32x2 lo = ld_tr16(v), hi = ld_tr16(v + 8 * L::VROW);
         return as_bf16x8(u32x4{lo.x, lo.y, hi.x, hi.y});
     };
-    const auto scores = [&](Scores &x, int buf) {
-#pragma unroll
-        for (int i = 0; i < SK; ++i) {
-            if (i < 2) x.s[i] = f32x16{};
-            x.s[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_part(buf, i), q[i / 2], x.s[i % 2], 0, 0, 0);
-        }
+    const auto k_step = [&](Scores &x, int i, bf16x8 part) {
+        if (i < 2) x.s[i] = f32x16{};
+        x.s[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part, q[i / 2], x.s[i % 2], 0, 0, 0);
     };
-    // Word w of the weights: scores 2w and 2w + 1.
-    const auto weight = [&](const Scores &x, float base, int w) {
-        const float y = exp2_fast(__builtin_fmaf(x.s[w / 8][2 * w % 16], a.scale, -base));
-        const float z = exp2_fast(__builtin_fmaf(x.s[w / 8][2 * w % 16 + 1], a.scale, -base));
-        sum += y + z;
-        return pack_bf16x2(y, z);
+    struct Weights {
+        u32x4 p[4];
     };
-    const auto largest = [&](const Scores &x) {
-        float top = x.s[0][0];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, x.s[t][e]);
-        return top;
+    const auto v_step = [&](const Weights &w, int i, bf16x8 part) {
+        const int t = i % (D / 32), g = i / (D / 32);
+        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part, as_bf16x8(w.p[g]), acc[t], 0, 0, 0);
+    };
+    // Word i of the weights: scores 2i and 2i + 1.
+    const auto weigh = [&](const Scores &x, float base, Weights &w, int i) {
+        const float y = exp2_fast(__builtin_fmaf(x.s[i / 8][2 * i % 16], a.scale, -base));
+        const float z = exp2_fast(__builtin_fmaf(x.s[i / 8][2 * i % 16 + 1], a.scale, -base));
+        sum = here(sum + (y + z));
+        w.p[i / 4][i % 4] = here(pack_bf16x2(y, z));
+    };
+    const auto larger = [&](const Scores &x, float top, int i) {
+        return here(__builtin_fmaxf(top, __builtin_fmaxf(x.s[i / 8][2 * i % 16], x.s[i / 8][2 * i % 16 + 1])));
     };
     // Masks the scores of an edge and raises the reference where they exceed it.
     const auto settle = [&](Scores &x, float top, int t0, bool edge) {
         if (edge) {
+            top = kNegInf;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const int k = t0 + 32 * t + 8 * (e / 4) + 4 * half + e % 4;
-                    const bool on = k <= pos && (a.window == 0 || k > pos - a.window || k < a.sinks);
+                    const bool on = (k <= pos) & ((a.window == 0) | (k > pos - a.window) | (k < a.sinks));
                     x.s[t][e] = on ? x.s[t][e] : kNegInf;
+                    top = __builtin_fmaxf(top, x.s[t][e]);
                 }
-            top = largest(x);
         }
         top *= a.scale;
         if (__any(top > ref + 8.0f)) {
@@ -321,101 +318,107 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     };
     if (tid == 0) s_odd = s_bad = 0;
     __syncthreads();
-    // K runs a tile ahead of V: the scores of the next tile are computed next to
-    // the exponentials of this one.
+    // K runs a tile ahead of V in LDS: the scores of the next tile are computed
+    // next to the exponentials of this one.
     if (u0 < u1) {
-        const auto load_k = [&](int t0) {
-#pragma unroll
-            for (int i = 0; i < L::ITEMS; ++i) load(i, k_head, ks_head, t0, entry);
-        };
-        const auto move_on = [&](int t0) {
-#pragma unroll
-            for (int i = 0; i < L::ITEMS; ++i) {
-                entry_v[i] = entry[i];
-                look_up(i, t0);
-            }
-        };
-        const auto load_v = [&](int t0) {
-#pragma unroll
-            for (int i = 0; i < L::ITEMS; ++i) load(i, v_head, vs_head, t0, entry_v);
-        };
         const int t0 = tile_token(u0);
-        int t1 = token_after(t0), t2 = token_after(t1);  // of the next two tiles
-        move_on(t0);
-        load_k(t0);
-        store_k(0);
-        move_on(t1);
-        load_v(t0);
-        store_v(t0, is_edge(t0), 0);
-        load_k(t1);
-        move_on(t2);
-        store_k(1);
+        int t1 = token_after(t0), t2 = token_after(t1);  // the next two tiles
+        Entries e0, e1;
+        const auto look_up_all = [&](int t, Entries &e) {
+#pragma unroll
+            for (int i = 0; i < L::ITEMS; ++i) look_up(i, t, e);
+        };
+        const auto load_all = [&](const uint8_t *elements, const uint8_t *scales, int t, const Entries &e, Items &r) {
+#pragma unroll
+            for (int i = 0; i < L::ITEMS; ++i) load(i, elements, scales, t, e, r);
+        };
+        look_up_all(t0, e0);
+        look_up_all(t1, e1);
+        load_all(k_head, ks_head, t0, e0, rk);
+        load_all(v_head, vs_head, t0, e0, rv);
+#pragma unroll
+        for (int i = 0; i < L::ITEMS; ++i) store_k(i, 0);
+        load_all(k_head, ks_head, t1, e1, rk);
+#pragma unroll
+        for (int i = 0; i < L::ITEMS; ++i) store_v(i, t0, is_edge(t0), 0);
+        look_up_all(t2, e0);
+        load_all(v_head, vs_head, t1, e1, rv);
+#pragma unroll
+        for (int i = 0; i < L::ITEMS; ++i) store_k(i, 1);
         __syncthreads();
         Scores s0, s1;
-        scores(s0, 0);
-        settle(s0, largest(s0), t0, is_edge(t0));
+        float top = kNegInf;
+#pragma unroll
+        for (int i = 0; i < SK; ++i) k_step(s0, i, k_part(0, i));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = larger(s0, top, i);
+        settle(s0, top, t0, is_edge(t0));
         __syncthreads();  // the first turn overwrites the first K
-        // One tile: its scores are in x, the next one's go to y. The order of the
-        // steps is kept by the scheduling barriers: next to each matrix product
-        // of K stand a pair's exponentials, next to V's a piece of the maximum,
-        // and the operands are read AHEAD steps before their use.
-        const auto turn = [&](int buf, Scores &x, Scores &y) {
-            load_v(t1);
+        // One tile: its scores are in x, the next one's go to y; e holds the page
+        // entries of tile t2, f gets those of the one after it. The vector work
+        // is spread evenly over the products' steps, whose order the scheduling
+        // barriers keep: two waves share a SIMD, and where both are in a part
+        // with much of it the matrix core waits. Next to the products with K
+        // stand the first EARLY words of the weights and K's loads, next to
+        // V's the other words, then the maximum, the stores to LDS and V's
+        // loads. Operands are read AHEAD steps before their use.
+        constexpr int EARLY = 10, HALF = SV / 2;
+        const auto turn = [&](int buf, Scores &x, Scores &y, Entries &e, Entries &f) {
             const int t3 = token_after(t2);
             const bool edge = is_edge(t1);
             const float base = ref == kNegInf ? 0.0f : ref;
-            u32x4 p[4];
+            Weights w;
             bf16x8 part[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) part[i] = k_part(buf ^ 1, i);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < SK; ++i) {
-                if (i < 2) y.s[i] = f32x16{};
-                y.s[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part[i % AHEAD], q[i / 2], y.s[i % 2], 0, 0, 0);
+                k_step(y, i, part[i % AHEAD]);
                 part[i % AHEAD] = i + AHEAD < SK ? k_part(buf ^ 1, i + AHEAD) : v_part(buf, i + AHEAD - SK);
+                if (i < L::ITEMS) look_up(i, t3, f);
+                else if (i < 2 * L::ITEMS) load(i - L::ITEMS, k_head, ks_head, t2, e, rk);
 #pragma unroll
-                for (int w = 16 * i / SK; w < 16 * (i + 1) / SK; ++w) p[w / 4][w % 4] = here(weight(x, base, w));
-                sum = here(sum);
+                for (int k = EARLY * i / SK; k < EARLY * (i + 1) / SK; ++k) weigh(x, base, w, k);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            store_v(t1, edge, buf ^ 1);
-            load_k(t2);
-            move_on(t3);
-            __builtin_amdgcn_sched_barrier(0);
-            float top = y.s[0][0];
+            float top = kNegInf;
 #pragma unroll
             for (int i = 0; i < SV; ++i) {
-                const int t = i % (D / 32), g = i / (D / 32);
-                acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part[i % AHEAD], as_bf16x8(p[g]), acc[t], 0, 0, 0);
+                v_step(w, i, part[i % AHEAD]);
                 if (i + AHEAD < SV) part[i % AHEAD] = v_part(buf, i + AHEAD);
+                if (i < HALF) {
 #pragma unroll
-                for (int w = 16 * i / SV; w < 16 * (i + 1) / SV; ++w)
-                    top = here(__builtin_fmaxf(top, __builtin_fmaxf(y.s[w / 8][2 * w % 16], y.s[w / 8][2 * w % 16 + 1])));
+                    for (int k = EARLY + (16 - EARLY) * i / HALF; k < EARLY + (16 - EARLY) * (i + 1) / HALF; ++k) weigh(x, base, w, k);
+                } else {
+#pragma unroll
+                    for (int k = 16 * (i - HALF) / HALF; k < 16 * (i + 1 - HALF) / HALF; ++k) top = larger(y, top, k);
+                    const int j = i - HALF;  // HALF is 4 * ITEMS, or 3 * ITEMS at 96
+                    if (j < L::ITEMS) store_v(j, t1, edge, buf ^ 1);
+                    else if (j < 2 * L::ITEMS) load(j - L::ITEMS, v_head, vs_head, t2, e, rv);
+                    else if (j < 3 * L::ITEMS) store_k(j - 2 * L::ITEMS, buf);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            store_k(buf);
             settle(y, top, t1, edge);
             t1 = t2, t2 = t3;
             __syncthreads();
         };
         const auto last = [&](int buf, Scores &x) {
             const float base = ref == kNegInf ? 0.0f : ref;
-            u32x4 p[4];
+            Weights w;
 #pragma unroll
-            for (int w = 0; w < 16; ++w) p[w / 4][w % 4] = weight(x, base, w);
+            for (int i = 0; i < 16; ++i) weigh(x, base, w, i);
 #pragma unroll
-            for (int i = 0; i < SV; ++i)
-                acc[i % (D / 32)] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_part(buf, i), as_bf16x8(p[i / (D / 32)]),
-                                                                            acc[i % (D / 32)], 0, 0, 0);
+            for (int i = 0; i < SV; ++i) v_step(w, i, v_part(buf, i));
         };
         int u = u0;
         for (; u + 2 < u1; u += 2) {
-            turn(0, s0, s1);
-            turn(1, s1, s0);
+            turn(0, s0, s1, e0, e1);
+            turn(1, s1, s0, e1, e0);
         }
         if (u + 1 < u1) {
-            turn(0, s0, s1);
+            turn(0, s0, s1, e0, e1);
             last(1, s1);
         } else {
             last(0, s0);
@@ -532,7 +535,7 @@ hipError_t launch(const PrefillArgs &a, dim3 grid, hipStream_t s) {
     const unsigned join = (unsigned)((total + 3) / 4);
 #define QBN_KV_DIM(DD)                                                         \
     case DD:                                                                   \
-        k_prefill<F, DD, 4><<<grid, 256, 0, s>>>(a);                           \
+        k_prefill<F, DD><<<grid, 256, 0, s>>>(a);                              \
         if (a.splits > 1) k_prefill_join<DD><<<join, 256, 0, s>>>(a, total);   \
         break;
     switch (a.dim) {
