@@ -41,9 +41,9 @@ struct PrefillArgs {
     int group, window, sinks, splits, dim;
 };
 
-template <int F, int D>
+template <int F, int D, int NW>
 struct Lay {
-    static constexpr int NW = 4, NT = NW * 64, BM = NW * 32;
+    static constexpr int NT = NW * 64, BM = NW * 32;
     // Bytes of a row in LDS (64 banks, 16 pieces of 16 bytes): an odd number of
     // pieces, so that sixteen rows' same piece lie in all banks, and 4 or 12
     // pieces (mod 16), so that four rows' 64 bytes do.
@@ -84,13 +84,13 @@ __device__ __forceinline__ float element(const Cache &c, int64_t head, int ps, i
     return __uint_as_float(o[0] << 16);
 }
 
-template <int F, int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a) {
-    using L = Lay<F, D>;
+template <int F, int D, int NW>
+__global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a) {
+    using L = Lay<F, D, NW>;
     __shared__ __align__(16) uint8_t s_k[2][L::KBUF], s_v[2][L::VBUF];
     __shared__ int s_odd;  // a tile that not every row sees held an infinity or NaN of V
     __shared__ int s_bad;  // a visible token's table entry was no page
-    __shared__ int64_t s_scan[L::NW + 1];
+    __shared__ int64_t s_scan[NW + 1];
     __shared__ int s_at[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, half = lane >> 5;
@@ -281,12 +281,24 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a
         const int t = i % (D / 32), g = i / (D / 32);
         acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(part, as_bf16x8(w.p[g]), acc[t], 0, 0, 0);
     };
-    // Word i of the weights: scores 2i and 2i + 1.
-    const auto weigh = [&](const Scores &x, float base, Weights &w, int i) {
-        const float y = exp2_fast(__builtin_fmaf(x.s[i / 8][2 * i % 16], a.scale, -base));
-        const float z = exp2_fast(__builtin_fmaf(x.s[i / 8][2 * i % 16 + 1], a.scale, -base));
-        sum = here(sum + (y + z));
-        w.p[i / 4][i % 4] = here(pack_bf16x2(y, z));
+    // Word k of the weights is made of scores 2k and 2k + 1, in three ticks, so
+    // that nothing waits for the exponential before it: tick k scales the
+    // scores, tick k + 1 takes the powers, tick k + 2 adds and rounds.
+    float arg[2][2], pow[2][2];
+    const auto tick = [&](const Scores &x, float base, Weights &w, int k) {
+        if (k >= 1 && k <= 16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pow[(k - 1) % 2][i] = here(exp2_fast(arg[(k - 1) % 2][i]));
+        }
+        if (k >= 2) {
+            const float y = pow[k % 2][0], z = pow[k % 2][1];
+            sum = here(sum + (y + z));
+            w.p[(k - 2) / 4][(k - 2) % 4] = here(pack_bf16x2(y, z));
+        }
+        if (k < 16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) arg[k % 2][i] = here(__builtin_fmaf(x.s[k / 8][2 * k % 16 + i], a.scale, -base));
+        }
     };
     const auto larger = [&](const Scores &x, float top, int i) {
         return here(__builtin_fmaxf(top, __builtin_fmaxf(x.s[i / 8][2 * i % 16], x.s[i / 8][2 * i % 16 + 1])));
@@ -359,10 +371,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a
         // is spread evenly over the products' steps, whose order the scheduling
         // barriers keep: two waves share a SIMD, and where both are in a part
         // with much of it the matrix core waits. Next to the products with K
-        // stand the first EARLY words of the weights and K's loads, next to
-        // V's the other words, then the maximum, the stores to LDS and V's
+        // stand the first EARLY ticks of the weights and K's loads, next to
+        // V's the other ticks, then the maximum, the stores to LDS and V's
         // loads. Operands are read AHEAD steps before their use.
-        constexpr int EARLY = 10, HALF = SV / 2;
+        constexpr int TICKS = 18, EARLY = 11, HALF = SV / 2;
         const auto turn = [&](int buf, Scores &x, Scores &y, Entries &e, Entries &f) {
             const int t3 = token_after(t2);
             const bool edge = is_edge(t1);
@@ -379,7 +391,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a
                 if (i < L::ITEMS) look_up(i, t3, f);
                 else if (i < 2 * L::ITEMS) load(i - L::ITEMS, k_head, ks_head, t2, e, rk);
 #pragma unroll
-                for (int k = EARLY * i / SK; k < EARLY * (i + 1) / SK; ++k) weigh(x, base, w, k);
+                for (int k = EARLY * i / SK; k < EARLY * (i + 1) / SK; ++k) tick(x, base, w, k);
                 __builtin_amdgcn_sched_barrier(0);
             }
             float top = kNegInf;
@@ -389,7 +401,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a
                 if (i + AHEAD < SV) part[i % AHEAD] = v_part(buf, i + AHEAD);
                 if (i < HALF) {
 #pragma unroll
-                    for (int k = EARLY + (16 - EARLY) * i / HALF; k < EARLY + (16 - EARLY) * (i + 1) / HALF; ++k) weigh(x, base, w, k);
+                    for (int k = EARLY + (TICKS - EARLY) * i / HALF; k < EARLY + (TICKS - EARLY) * (i + 1) / HALF; ++k)
+                        tick(x, base, w, k);
                 } else {
 #pragma unroll
                     for (int k = 16 * (i - HALF) / HALF; k < 16 * (i + 1 - HALF) / HALF; ++k) top = larger(y, top, k);
@@ -408,7 +421,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_prefill(PrefillArgs a
             const float base = ref == kNegInf ? 0.0f : ref;
             Weights w;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) weigh(x, base, w, i);
+            for (int k = 0; k < TICKS; ++k) tick(x, base, w, k);
 #pragma unroll
             for (int i = 0; i < SV; ++i) v_step(w, i, v_part(buf, i));
         };
@@ -507,13 +520,14 @@ __global__ __launch_bounds__(256) void k_prefill_join(PrefillArgs a, int64_t tot
 
 struct Plan {
     int64_t tiles;  // row tiles at most
-    int splits;
+    int splits, waves;
 };
 
 Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
-    constexpr int BM = 128;
     Plan p;
     const int64_t group = q_heads / c.heads;
+    p.waves = c.head_dim <= 128 && b.tokens * group / 256 * c.heads >= 256 ? 8 : 4;
+    const int BM = p.waves * 32;
     p.tiles = b.cu ? b.tokens * group / BM + b.seqs : b.seqs * ((group + BM - 1) / BM);
     int64_t units = (b.row * c.page_size + BN - 1) / BN;
     if (window > 0) {
@@ -530,12 +544,13 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
 }
 
 template <int F>
-hipError_t launch(const PrefillArgs &a, dim3 grid, hipStream_t s) {
+hipError_t launch(const PrefillArgs &a, dim3 grid, int waves, hipStream_t s) {
     const int64_t total = (int64_t)a.b.tokens * a.c.heads * a.group;
     const unsigned join = (unsigned)((total + 3) / 4);
 #define QBN_KV_DIM(DD)                                                         \
     case DD:                                                                   \
-        k_prefill<F, DD><<<grid, 256, 0, s>>>(a);                              \
+        if (DD <= 128 && waves == 8) k_prefill<F, DD, DD <= 128 ? 8 : 4><<<grid, 512, 0, s>>>(a); \
+        else k_prefill<F, DD, 4><<<grid, 256, 0, s>>>(a);                      \
         if (a.splits > 1) k_prefill_join<DD><<<join, 256, 0, s>>>(a, total);   \
         break;
     switch (a.dim) {
@@ -575,8 +590,8 @@ hipError_t launch_kv_prefill(const qbn_kv_cache &c, int64_t layer, const qbn_kv_
     a.q_flip = scale < 0.0f ? 0x80008000u : 0u;
     a.group = q_heads / c.heads, a.window = window, a.sinks = sinks, a.splits = p.splits, a.dim = c.head_dim;
     const dim3 grid((unsigned)(p.tiles * c.heads), (unsigned)p.splits);
-    if (c.format == QBN_KV_BF16) return launch<BF16>(a, grid, s);
-    return c.format == QBN_MXFP8 ? launch<FP8>(a, grid, s) : launch<FP4>(a, grid, s);
+    if (c.format == QBN_KV_BF16) return launch<BF16>(a, grid, p.waves, s);
+    return c.format == QBN_MXFP8 ? launch<FP8>(a, grid, p.waves, s) : launch<FP4>(a, grid, p.waves, s);
 }
 
 }  // namespace qbn
