@@ -90,44 +90,38 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     __shared__ __align__(16) uint8_t s_k[2][L::KBUF], s_v[2][L::VBUF];
     __shared__ int s_odd;  // a tile that not every row sees held an infinity or NaN of V
     __shared__ int s_bad;  // a visible token's table entry was no page
-    __shared__ int64_t s_scan[NW + 1];
-    __shared__ int s_at[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, half = lane >> 5;
     const int kv_head = blockIdx.x % a.c.heads;
     const int want = blockIdx.x / a.c.heads;  // row tile in the list of all sequences'
 
-    // ---- which sequence and row tile
-    {
-        const int each = (a.b.seqs + L::NT - 1) / L::NT;
-        int64_t mine = 0;
-        int first;
-        for (int i = 0; i < each; ++i) {
-            const int s = tid * each + i;
-            if (s < a.b.seqs) mine += ((int64_t)new_tokens(a.b, s, first) * a.group + L::BM - 1) / L::BM;
+    // ---- which sequence and row tile: each wave scans the sequences for itself, 64 at a time
+    int b, tile, q0, fresh, len;
+    for (int64_t before = 0, s0 = 0;; s0 += 64) {
+        if (s0 >= a.b.seqs) return;
+        const int s = (int)s0 + lane;
+        int x = 0, n = 0, l = 0;
+        if (s < a.b.seqs) {
+            n = new_tokens(a.b, s, x);
+            l = a.b.lens[s];
         }
-        int64_t total;
-        int64_t before = block_scan<L::NT>(mine, s_scan, total);
-        if (want >= total) return;
-        if (before <= want && want < before + mine) {
-            for (int i = 0; i < each; ++i) {
-                const int s = tid * each + i;
-                const int64_t t = ((int64_t)new_tokens(a.b, s, first) * a.group + L::BM - 1) / L::BM;
-                if (want < before + t) {
-                    s_at[0] = s;
-                    s_at[1] = (int)(before + t - 1 - want);  // the longest rows first
-                    break;
-                }
-                before += t;
-            }
+        const int tiles = (int)(((int64_t)n * a.group + L::BM - 1) / L::BM);  // < 2^24
+        const int upto = wave_scan(tiles);
+        const uint64_t here = __ballot(want < before + upto);
+        if (here == 0) {
+            before += __builtin_amdgcn_readlane(upto, 63);
+            continue;
         }
-        __syncthreads();
+        const int at = __builtin_ctzll(here);
+        b = (int)s0 + at;
+        tile = (int)(before + __builtin_amdgcn_readlane(upto, at) - 1 - want);  // the longest rows first
+        q0 = __builtin_amdgcn_readlane(x, at);
+        fresh = __builtin_amdgcn_readlane(n, at);
+        len = __builtin_amdgcn_readlane(l, at);
+        break;
     }
-    const int b = __builtin_amdgcn_readfirstlane(s_at[0]), tile = __builtin_amdgcn_readfirstlane(s_at[1]);
-    int q0;
-    const int fresh = new_tokens(a.b, b, q0), rows = fresh * a.group;
+    const int rows = fresh * a.group;
     const int r0 = tile * L::BM;
-    int len = a.b.lens[b];
     const int ps = 1 << a.c.page_shift;
     const bool bad = len < 0 || (((int64_t)len + ps - 1) >> a.c.page_shift) > a.b.row;
     if (bad) len = 0;
