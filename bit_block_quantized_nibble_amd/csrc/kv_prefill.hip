@@ -215,11 +215,11 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 #pragma unroll
         for (int e = 0; e < 2; ++e) *reinterpret_cast<u32x4 *>(d + 16 * e) = u32x4{x[e][0], x[e][1], x[e][2], x[e][3]};
     };
-    const auto store_k = [&](int i, int buf) {
+    const auto store_k = [&](const Items &r, int i, int buf) {
         int t, blk;
         item(i, t, blk);
         uint32_t x[2][4];
-        expand_item(rk, i, x);
+        expand_item(r, i, x);
         put(s_k[buf] + t * L::KROW + blk * 32, x);
     };
     const auto store_v = [&](int i, int t0, bool edge, int buf) {
@@ -340,17 +340,18 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         };
         look_up_all(t0, e0);
         look_up_all(t1, e1);
-        load_all(k_head, ks_head, t0, e0, rk);
+        Items k0;
+        load_all(k_head, ks_head, t0, e0, k0);
         load_all(v_head, vs_head, t0, e0, rv);
-#pragma unroll
-        for (int i = 0; i < L::ITEMS; ++i) store_k(i, 0);
         load_all(k_head, ks_head, t1, e1, rk);
 #pragma unroll
-        for (int i = 0; i < L::ITEMS; ++i) store_v(i, t0, is_edge(t0), 0);
+        for (int i = 0; i < L::ITEMS; ++i) {
+            store_k(k0, i, 0);
+            store_v(i, t0, is_edge(t0), 0);
+            store_k(rk, i, 1);
+        }
         look_up_all(t2, e0);
         load_all(v_head, vs_head, t1, e1, rv);
-#pragma unroll
-        for (int i = 0; i < L::ITEMS; ++i) store_k(i, 1);
         __syncthreads();
         Scores s0, s1;
         float top = kNegInf;
@@ -403,7 +404,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
                     const int j = i - HALF;  // HALF is 4 * ITEMS, or 3 * ITEMS at 96
                     if (j < L::ITEMS) store_v(j, t1, edge, buf ^ 1);
                     else if (j < 2 * L::ITEMS) load(j - L::ITEMS, v_head, vs_head, t2, e, rv);
-                    else if (j < 3 * L::ITEMS) store_k(j - 2 * L::ITEMS, buf);
+                    else if (j < 3 * L::ITEMS) store_k(rk, j - 2 * L::ITEMS, buf);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -487,29 +488,46 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     }
 }
 
-// Joins the pieces of a split length, in order: a wave per row.
+// Joins the pieces of a split length, in order: D / 4 lanes per row, eight
+// pieces in flight. Bound by the pieces' bytes.
 template <int D>
 __global__ __launch_bounds__(256) void k_prefill_join(PrefillArgs a, int64_t total) {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= total) return;
+    constexpr int L = D / 4, ROWS = 64 / L;  // lanes of a row, rows of a wave
+    const int lane = threadIdx.x & 63, d = lane % L * 4;
+    const int64_t row = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * ROWS + lane / L;
+    if (lane >= ROWS * L || row >= total) return;
     const float *st = a.parts + total * a.splits * D;
-    float top = kNegInf;
-    for (int i = 0; i < a.splits; ++i) top = __builtin_fmaxf(top, st[i * total + row]);
-    constexpr int PER = (D + 63) / 64;
-    float o[PER] = {}, sum = 0.0f;
-    for (int i = 0; i < a.splits; ++i) {
-        const float ri = st[i * total + row], f = ri == top ? 1.0f : exp2_fast(ri - top);
-        sum += f * st[(a.splits + i) * total + row];
+    float top = kNegInf, sum = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    for (int i0 = 0; i0 < a.splits; i0 += 8) {
+        f32x4 v[8];
+        float r[8], s[8];
 #pragma unroll
-        for (int e = 0; e < PER; ++e)
-            if (D % 64 == 0 || e * 64 + lane < D) o[e] += f * a.parts[(i * total + row) * D + e * 64 + lane];
+        for (int k = 0; k < 8; ++k) {
+            const int64_t at = min(i0 + k, a.splits - 1) * total + row;
+            v[k] = *reinterpret_cast<const f32x4 *>(a.parts + at * D + d);
+            r[k] = st[at];
+            s[k] = st[a.splits * total + at];
+        }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) now = __builtin_fmaxf(now, r[k]);
+        const float f = top == now ? 1.0f : exp2_fast(top - now);
+        o *= f;
+        sum *= f;
+        top = now;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (i0 + k < a.splits) {
+                const float w = r[k] == top ? 1.0f : exp2_fast(r[k] - top);
+                o += v[k] * w;
+                sum += s[k] * w;
+            }
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int e = 0; e < PER; ++e)
-        if (D % 64 == 0 || e * 64 + lane < D) a.out[row * D + e * 64 + lane] = (__bf16)(o[e] * inv);
-    if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    *reinterpret_cast<u32x2 *>(a.out + row * D + d) = u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+    if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 struct Plan {
@@ -530,9 +548,9 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
     }
     const int64_t blocks = p.tiles * c.heads;
     // Few row tiles: the length is split until about two workgroups per
-    // compute unit run, each with at least eight tiles of 64 tokens.
+    // compute unit run, each with at least four tiles of 64 tokens.
     int64_t splits = blocks > 0 && blocks < 512 ? 512 / blocks : 1;
-    if (splits > units / 8) splits = units / 8;
+    if (splits > units / 4) splits = units / 4;
     p.splits = (int)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
     return p;
 }
@@ -540,12 +558,14 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
 template <int F>
 hipError_t launch(const PrefillArgs &a, dim3 grid, int waves, hipStream_t s) {
     const int64_t total = (int64_t)a.b.tokens * a.c.heads * a.group;
-    const unsigned join = (unsigned)((total + 3) / 4);
 #define QBN_KV_DIM(DD)                                                         \
     case DD:                                                                   \
         if (DD <= 128 && waves == 8) k_prefill<F, DD, DD <= 128 ? 8 : 4><<<grid, 512, 0, s>>>(a); \
         else k_prefill<F, DD, 4><<<grid, 256, 0, s>>>(a);                      \
-        if (a.splits > 1) k_prefill_join<DD><<<join, 256, 0, s>>>(a, total);   \
+        if (a.splits > 1) {                                                    \
+            constexpr int per = 4 * (256 / DD);                                \
+            k_prefill_join<DD><<<(unsigned)((total + per - 1) / per), 256, 0, s>>>(a, total); \
+        }                                                                      \
         break;
     switch (a.dim) {
         QBN_KV_DIM(64)
