@@ -548,9 +548,9 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
     }
     const int64_t blocks = p.tiles * c.heads;
     // Few row tiles: the length is split until about two workgroups per
-    // compute unit run, each with at least four tiles of 64 tokens.
+    // compute unit run, each with at least two tiles of 64 tokens.
     int64_t splits = blocks > 0 && blocks < 512 ? 512 / blocks : 1;
-    if (splits > units / 4) splits = units / 4;
+    if (splits > units / 2) splits = units / 2;
     p.splits = (int)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
     return p;
 }
