@@ -85,21 +85,23 @@ __device__ __forceinline__ Chunk scan_of(int n) {
     c.all = __builtin_amdgcn_readlane(c.upto, 63);
     return c;
 }
-__device__ __forceinline__ int units_of(const DecodeArgs &a, int s0) {
+__device__ __forceinline__ int length_at(const DecodeArgs &a, int s0) {  // of this lane's sequence
     const int s = s0 + (threadIdx.x & 63);
-    return s < a.b.seqs ? span_of(a, a.b.lens[s]).n : 0;  // < 2^24
+    return s < a.b.seqs ? a.b.lens[s] : 0;
 }
-__device__ __forceinline__ uint32_t pieces_of(uint32_t n, uint32_t per) { return (n + per - 1) / per; }
+__device__ __forceinline__ uint32_t pieces_of(const DecodeArgs &a, int len, uint32_t per) {
+    return ((uint32_t)span_of(a, len).n + per - 1) / per;
+}
 
 struct Plan {
-    int first;     // units of sequences 0 .. 63, one per lane
+    int first;     // lengths of sequences 0 .. 63, one per lane
     uint32_t per;  // units of a piece at most
 };
 __device__ __forceinline__ Plan plan_units(const DecodeArgs &a) {
     Plan p;
-    p.first = units_of(a, 0);
-    int64_t total = scan_of(p.first).all;
-    for (int s = 64; s < a.b.seqs; s += 64) total += scan_of(units_of(a, s)).all;
+    p.first = length_at(a, 0);
+    int64_t total = scan_of(span_of(a, p.first).n).all;  // a sequence has less than 2^24 units
+    for (int s = 64; s < a.b.seqs; s += 64) total += scan_of(span_of(a, length_at(a, s)).n).all;
     const int64_t per = div_i64(total * a.rows + a.blocks - 1, a.blocks);
     p.per = (uint32_t)(per < 1 ? 1 : per < (1 << 24) ? per : 1 << 24);
     return p;
@@ -298,23 +300,27 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // ---- this workgroup's piece
-    int b, r, piece = 0, pieces = 1;
+    int b, r, len, piece = 0, pieces = 1;
     if (a.parts == nullptr) {  // one workgroup per pair
         b = blockIdx.x / a.rows;
         r = blockIdx.x % a.rows;
+        len = length_of(a.b, b);
     } else {
         const Plan p = plan_units(a);
-        Chunk c = scan_of(pieces_of(p.first, p.per));
+        int lens = p.first;
+        Chunk c = scan_of(pieces_of(a, lens, p.per));
         int64_t before = 0;
         int s0 = 0;
         while (blockIdx.x >= (before + c.all) * a.rows) {
             before += c.all;
             s0 += 64;
             if (s0 >= a.b.seqs) return;  // more workgroups than pieces
-            c = scan_of(pieces_of(units_of(a, s0), p.per));
+            lens = length_at(a, s0);
+            c = scan_of(pieces_of(a, lens, p.per));
         }
         const int at = __builtin_ctzll(__ballot(blockIdx.x < (before + c.upto) * a.rows));
         b = s0 + at;
+        len = __builtin_amdgcn_readlane(lens, at);
         pieces = __builtin_amdgcn_readlane(c.n, at);
         const uint32_t rest = (uint32_t)(blockIdx.x - (before + __builtin_amdgcn_readlane(c.upto, at) - pieces) * a.rows);
         r = rest / pieces;
@@ -327,7 +333,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
     w.g = lane >> 4;
     w.b = __builtin_amdgcn_readfirstlane(b);
     w.kv_head = __builtin_amdgcn_readfirstlane(r / a.tiles);
-    w.sp = span_of(a, length_of(a.b, w.b));
+    w.sp = span_of(a, __builtin_amdgcn_readfirstlane(len));
     const int h0 = r % a.tiles * 16, heads = min(16, a.group - h0);
     const int hq = w.kv_head * a.group + h0;  // first query head of the pair
     const int u0 = (int)((int64_t)w.sp.n * piece / pieces), u1 = (int)((int64_t)w.sp.n * (piece + 1) / pieces);
@@ -441,10 +447,10 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a) {
     // pieces before this sequence, and its own
     const Plan p = plan_units(a);
     int64_t before = 0;
-    Chunk c = scan_of(pieces_of(p.first, p.per));
+    Chunk c = scan_of(pieces_of(a, p.first, p.per));
     for (int s = 64; s <= b; s += 64) {
         before += c.all;
-        c = scan_of(pieces_of(units_of(a, s), p.per));
+        c = scan_of(pieces_of(a, length_at(a, s), p.per));
     }
     const int count = __builtin_amdgcn_readlane(c.n, b & 63);
     before += __builtin_amdgcn_readlane(c.upto, b & 63) - count;
