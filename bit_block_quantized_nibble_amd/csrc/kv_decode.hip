@@ -50,7 +50,8 @@ struct DecodeArgs {
     __bf16 *out;
     float *lse;
     float *parts;  // pieces: [16][D] sums, then [16] maxima and [16] sums of weights
-    float scale;   // times log2 e
+    float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
+    uint32_t q_keep, q_flip;
     int group, tiles, rows;  // query heads per key-value head, 16-row tiles of them, pairs per sequence
     int window, sinks, blocks, dim;
 };
@@ -127,73 +128,87 @@ struct Tile {
 template <int F, int D>
 struct Decoder {
     using T = Tile<F, D>;
+    static constexpr int ROW = D * kBits<F> / 8;  // bytes of a token's head
     const DecodeArgs &a;
-    int lane, m, g, kv_head, b;
+    int m, g, b;
     Span sp;
+    // K's and V's first bytes of this lane in page 0, at the first slot of a tile
+    const uint8_t *k, *v, *ks, *vs;
+    uint32_t page_rows;
     bool bad = false;
 
-    __device__ __forceinline__ bool sees(int t) const { return t < sp.len && (t >= sp.lo || t < a.sinks); }
+    __device__ __forceinline__ Decoder(const DecodeArgs &args, int lane, int seq, int kv_head, int len)
+        : a(args), m(lane & 15), g(lane >> 4), b(seq), sp(span_of(args, len)) {
+        const int ps = 1 << a.c.page_shift;
+        page_rows = (uint32_t)a.c.heads << a.c.page_shift;  // a page's bytes fit 32 bits
+        const int64_t head = (int64_t)kv_head << a.c.page_shift;
+        // K: rows 4g' + i of the first product are tokens 8g' + i, of the second 8g' + 4 + i
+        const int kt = (8 * (m / 4) + m % 4) & (ps - 1), vt = 8 * g & (ps - 1);
+        k = a.c.k + (head + kt) * ROW + g * T::KB;
+        v = a.c.v + (head + vt) * ROW;
+        ks = a.c.ks + head * (D / 32) + kt;
+        vs = a.c.vs + head * (D / 32) + vt;
+    }
+
+    __device__ __forceinline__ bool sees(int t) const { return (t < sp.len) & ((t >= sp.lo) | (t < a.sinks)); }
 
     // The pages of tokens t .. t + 15 and t + 16 .. t + 31 (t % 32 == 0): page 0
     // where none of them is seen.
     struct Pages {
-        int p[2];
+        uint32_t p[2];
     };
     __device__ __forceinline__ Pages pages_of(int t0) {
         Pages r;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = t0 + 16 * i;
-            const bool any = t < sp.len && (t + 15 >= sp.lo || t < a.sinks);
-            const int p = table_entry(a.b, b, any ? t >> a.c.page_shift : 0);
-            const bool page = (uint32_t)p < (uint32_t)a.c.pages;
-            bad |= any && !page;
-            r.p[i] = any && page ? p : 0;
+            const bool any = (t < sp.len) & ((t + 15 >= sp.lo) | (t < a.sinks));
+            const uint32_t p = table_entry(a.b, b, any ? t >> a.c.page_shift : 0);
+            const bool page = p < (uint32_t)a.c.pages;
+            bad |= any & !page;
+            r.p[i] = any & page ? p : 0;
         }
         return r;
     }
 
     __device__ __forceinline__ void load(T &r, int t0, Pages pages) {
         const int ps = 1 << a.c.page_shift;
-        const int64_t p0 = pages.p[0], p1 = pages.p[1];
-        // K: rows 4g' + i of the first product are tokens 8g' + i, of the second 8g' + 4 + i
+        const uint32_t slot = (uint32_t)t0 & (uint32_t)(ps - 1);  // 0 where a page holds half a tile
         {
-            const int t = 8 * (m / 4) + m % 4;  // < 16 for m < 8
-            const int64_t head = (m < 8 ? p0 : p1) * a.c.heads + kv_head;
-            const int slot = (t0 + t) & (ps - 1);
+            const uint32_t page = m < 8 ? pages.p[0] : pages.p[1];
+            const uint8_t *row = k + (uint64_t)page * (page_rows * ROW) + slot * ROW;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t *row = a.c.k + ((head * ps + slot + 4 * i) * D) * kBits<F> / 8;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int c = 0; c < T::NC; ++c) load_words<T::KB>(row + (c * 4 + g) * T::KB, r.k[i] + c * T::KW);
-                if constexpr (F != BF16) {
-                    const uint8_t *sc = a.c.ks + head * (D / 32) * ps + slot + 4 * i;
+                for (int c = 0; c < T::NC; ++c) load_words<T::KB>(row + 4 * i * ROW + c * 4 * T::KB, r.k[i] + c * T::KW);
+            if constexpr (F != BF16) {
+                const uint8_t *sc = ks + (uint64_t)page * (page_rows * (D / 32)) + slot;
 #pragma unroll
-                    for (int c = 0; c < T::NC; ++c) r.ks[i][c] = sc[(c * 4 + g) * T::E / 32 * ps];
+                for (int c = 0; c < T::NC; ++c) {
+                    const uint8_t *x = sc + (((c * 4 + g) * T::E / 32) << a.c.page_shift);
+                    r.ks[0][c] = x[0];
+                    r.ks[1][c] = x[4];
                 }
             }
         }
         {
-            const int64_t head = (g < 2 ? p0 : p1) * a.c.heads + kv_head;
-            const int slot = (t0 + 8 * g) & (ps - 1);
-            const uint8_t *row = a.c.v + ((head * ps + slot) * D) * kBits<F> / 8;
+            const uint32_t page = g < 2 ? pages.p[0] : pages.p[1];
+            const uint8_t *row = v + (uint64_t)page * (page_rows * ROW) + slot * ROW;
+            const uint8_t *r8 = row + m * kBits<F>, *r4 = row + (T::N8 * 128 + m * 4) * kBits<F> / 8,
+                          *r2 = row + (T::N8 * 128 + T::N4 * 64 + m * 2) * kBits<F> / 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint8_t *p = row + j * (D * kBits<F> / 8);
 #pragma unroll
-                for (int n = 0; n < T::N8; ++n) load_words<kBits<F>>(p + (n * 128 + m * 8) * kBits<F> / 8, r.v[j] + n * T::W8);
-                if constexpr (T::N4 > 0)
-                    load_words<4 * kBits<F> / 8>(p + (T::N8 * 128 + m * 4) * kBits<F> / 8, r.v[j] + T::N8 * T::W8);
-                if constexpr (T::N2 > 0)
-                    load_words<2 * kBits<F> / 8>(p + (T::N8 * 128 + T::N4 * 64 + m * 2) * kBits<F> / 8,
-                                                 r.v[j] + T::N8 * T::W8 + T::N4 * T::W4);
+                for (int n = 0; n < T::N8; ++n) load_words<kBits<F>>(r8 + j * ROW + n * 16 * kBits<F>, r.v[j] + n * T::W8);
+                if constexpr (T::N4 > 0) load_words<4 * kBits<F> / 8>(r4 + j * ROW, r.v[j] + T::N8 * T::W8);
+                if constexpr (T::N2 > 0) load_words<2 * kBits<F> / 8>(r2 + j * ROW, r.v[j] + T::N8 * T::W8 + T::N4 * T::W4);
             }
             if constexpr (F != BF16) {
-                const uint8_t *sc = a.c.vs + head * (D / 32) * ps + slot;
+                const uint8_t *sc = vs + (uint64_t)page * (page_rows * (D / 32)) + slot;
 #pragma unroll
-                for (int n = 0; n < T::N8; ++n) r.vs[n] = ld8(sc + (n * 4 + m / 4) * ps);
-                if constexpr (T::N4 > 0) r.vs[T::N8] = ld8(sc + (T::N8 * 4 + m / 8) * ps);
-                if constexpr (T::N2 > 0) r.vs[T::N8 + T::N4] = ld8(sc + (T::N8 * 4 + T::N4 * 2) * ps);
+                for (int n = 0; n < T::N8; ++n) r.vs[n] = ld8(sc + ((n * 4 + m / 4) << a.c.page_shift));
+                if constexpr (T::N4 > 0) r.vs[T::N8] = ld8(sc + ((T::N8 * 4 + m / 8) << a.c.page_shift));
+                if constexpr (T::N2 > 0) r.vs[T::N8 + T::N4] = ld8(sc + ((T::N8 * 4 + T::N4 * 2) << a.c.page_shift));
             }
         }
     }
@@ -222,7 +237,7 @@ struct Decoder {
         uint32_t c[8][W / 2];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float sc = F == BF16 ? 1.0f : e8m0_f32((j < 4 ? vs.x : vs.y) >> (8 * (j & 3)));
+            const float sc = F == BF16 ? 1.0f : e8m0_operand(j < 4 ? vs.x : vs.y, j & 3);
             expand<F, W>(r.v[j] + word, sc, c[j]);
         }
 #pragma unroll
@@ -238,7 +253,7 @@ struct Decoder {
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int c = 0; c < T::NC; ++c) {
-                const float sc = F == BF16 ? 1.0f : e8m0_f32(r.ks[i][F == BF16 ? 0 : c]);
+                const float sc = F == BF16 ? 1.0f : e8m0_operand(r.ks[i][F == BF16 ? 0 : c]);
 #pragma unroll
                 for (int e = 0; e < T::E / 8; ++e) {
                     uint32_t o[4];
@@ -249,7 +264,7 @@ struct Decoder {
             }
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = s[j / 4][j & 3] * a.scale;
+        for (int j = 0; j < 8; ++j) x[j] = s[j / 4][j & 3];
         if (!whole) {
             clear_unseen(r, t0);
 #pragma unroll
@@ -258,6 +273,7 @@ struct Decoder {
         float top = x[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[j]);
+        top *= a.scale;
         if (__any(top > ref + 8.0f)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 16));
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
@@ -272,7 +288,8 @@ struct Decoder {
         u32x4 p;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            const float p0 = exp2_fast(x[j] - base), p1 = exp2_fast(x[j + 1] - base);
+            const float p0 = exp2_fast(__builtin_fmaf(x[j], a.scale, -base));
+            const float p1 = exp2_fast(__builtin_fmaf(x[j + 1], a.scale, -base));
             sum += p0 + p1;
             p[j / 2] = pack_bf16x2(p0, p1);
         }
@@ -327,15 +344,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
         piece = rest % pieces;
     }
 
-    Decoder<F, D> w{a};
-    w.lane = lane;
-    w.m = lane & 15;
-    w.g = lane >> 4;
-    w.b = __builtin_amdgcn_readfirstlane(b);
-    w.kv_head = __builtin_amdgcn_readfirstlane(r / a.tiles);
-    w.sp = span_of(a, __builtin_amdgcn_readfirstlane(len));
+    const int kv_head = __builtin_amdgcn_readfirstlane(r / a.tiles);
+    Decoder<F, D> w(a, lane, __builtin_amdgcn_readfirstlane(b), kv_head, __builtin_amdgcn_readfirstlane(len));
     const int h0 = r % a.tiles * 16, heads = min(16, a.group - h0);
-    const int hq = w.kv_head * a.group + h0;  // first query head of the pair
+    const int hq = kv_head * a.group + h0;  // first query head of the pair
     const int u0 = (int)((int64_t)w.sp.n * piece / pieces), u1 = (int)((int64_t)w.sp.n * (piece + 1) / pieces);
     // Q as the right operand, in the element order of K's pieces
     bf16x8 q[D / 32];
@@ -344,6 +356,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
         const int d = (s * 8 / T::E * 4 + w.g) * T::E + s * 8 % T::E;
         u32x4 t = {0, 0, 0, 0};
         if (w.m < heads) t = ld16(a.q + (int64_t)w.b * a.qt + (int64_t)(hq + w.m) * a.qh + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = (t[i] & a.q_keep) ^ a.q_flip;
         q[s] = as_bf16x8(t);
     }
     f32x4 acc[D / 16];
@@ -584,7 +598,9 @@ hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_b
     a.qt = q.token_stride, a.qh = q.head_stride;
     a.out = (__bf16 *)out, a.lse = lse;
     a.parts = p.blocks ? (float *)ws : nullptr;
-    a.scale = scale * kLog2e;
+    a.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
+    a.q_keep = scale == 0.0f ? 0u : ~0u;
+    a.q_flip = scale < 0.0f ? 0x80008000u : 0u;
     a.group = q_heads / c.heads, a.tiles = p.tiles, a.rows = c.heads * p.tiles;
     a.window = window, a.sinks = sinks, a.blocks = (int)p.blocks, a.dim = c.head_dim;
     const int64_t grid = p.blocks ? most_pieces(p) : p.pairs;

@@ -28,9 +28,12 @@ struct Batch {
     const int32_t *table, *lens, *cu;
 };
 
-// E8M0 byte -> its power of two (0 -> 2^-127, a binary32 subnormal; 255 is NaN).
-__device__ __forceinline__ float e8m0_f32(uint32_t b) {
-    return __builtin_amdgcn_ldexpf(1.0f, e8m0_exponent(b));
+// The scale operand of the converts for E8M0 byte `j` of w. They take its
+// exponent bits, so the byte in their place serves for all 256 values (0 stands
+// for 2^-127 there, 255 gives NaN; every byte with every code was compared
+// with the value 2^(b - 127) as the operand).
+__device__ __forceinline__ float e8m0_operand(uint32_t w, int j = 0) {
+    return __uint_as_float(((w >> (8 * j)) & 0xFFu) << 23);
 }
 
 // Entry `i` of sequence b's table row, both the same in the whole wave. A scalar

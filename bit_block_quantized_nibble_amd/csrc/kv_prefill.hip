@@ -80,7 +80,7 @@ __device__ __forceinline__ float element(const Cache &c, int64_t head, int ps, i
     if constexpr (F == BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(c.v)[at] << 16);
     if constexpr (F == FP8) w[0] = c.v[at];
     if constexpr (F == FP4) w[0] = (c.v[at / 2] >> (4 * (d & 1))) & 15u;
-    expand<F == BF16 ? FP8 : F, 2>(w, e8m0_f32(c.vs[(head * (D / 32) + d / 32) * ps + slot]), o);
+    expand<F == BF16 ? FP8 : F, 2>(w, e8m0_operand(c.vs[(head * (D / 32) + d / 32) * ps + slot]), o);
     return __uint_as_float(o[0] << 16);
 }
 
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             r.sc[i] = scales[((blk / 2) << a.c.page_shift) + slot + (uint64_t)page * (page_rows * (D / 32))];
     };
     const auto expand_item = [&](const Items &r, int i, uint32_t (&x)[2][4]) {
-        const float f = F == BF16 ? 1.0f : e8m0_f32(r.sc[i]);
+        const float f = F == BF16 ? 1.0f : e8m0_operand(r.sc[i]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) expand8<F>(r.w[i] + e * (L::IW / 2), f, x[e]);
     };
