@@ -108,9 +108,14 @@ __device__ __forceinline__ Plan plan_units(const DecodeArgs &a) {
     return p;
 }
 
-// A wave's 32 tokens as loaded: K rows, V rows and their scales.
+// A wave's 32 tokens as loaded. A vector memory instruction takes a compute
+// unit's address unit 16 cycles whatever its width, so all loads but those of
+// a page entry are 16 bytes a lane where they can be: K's pieces are, V's and
+// the scales go through LDS (the wave's own part, no barrier), where the
+// narrow pieces that the matrix operands are made of cost a quarter.
 template <int F, int D>
 struct Tile {
+    static constexpr int ROW = D * kBits<F> / 8;  // bytes of a token's head
     // K: a lane group's contiguous piece of E elements, NC pieces per row
     static constexpr int E = F == FP4 ? (D % 128 == 0 ? 32 : D % 64 == 0 ? 16 : 8) : F == FP8 ? (D % 64 == 0 ? 16 : 8) : 8;
     static constexpr int NC = D / (4 * E);
@@ -118,36 +123,41 @@ struct Tile {
     // V: 16 lanes cover 128, 64 or 32 elements of a row
     static constexpr int N8 = D / 128, N4 = D % 128 / 64, N2 = D % 64 / 32, NS = N8 + N4 + N2;
     static constexpr int words(int w) { return w * kBits<F> / 32 > 0 ? w * kBits<F> / 32 : 1; }
-    static constexpr int W8 = words(8), W4 = words(4), W2 = words(2);
+    static constexpr int W8 = words(8), W4 = words(4), W2 = words(2), VW = N8 * W8 + N4 * W4 + N2 * W2;
+    static constexpr bool STAGED = F != BF16 || D % 128 != 0;  // otherwise V's pieces are 16 bytes already
+    static constexpr int CHUNKS = 2 * ROW, VN = (CHUNKS + 63) / 64;           // 16-byte chunks of 32 rows; loads
+    static constexpr int SCALES = F == BF16 ? 0 : D / 2, SN = (SCALES + 63) / 64;  // 4-byte words of K's and V's scales; loads
+    // In LDS: V's rows with 16 bytes of padding, then the scales [K, V][D / 32][32].
+    static constexpr int VROW = ROW + 16, SOFF = STAGED ? 32 * VROW : 0, BYTES = SOFF + 4 * SCALES;
     uint32_t k[2][NC * KW];
-    uint32_t ks[F == BF16 ? 1 : 2][F == BF16 ? 1 : NC];
-    uint32_t v[8][N8 * W8 + N4 * W4 + N2 * W2];
-    u32x2 vs[F == BF16 ? 1 : NS];
+    u32x4 v[STAGED ? VN : 8 * N8];
+    uint32_t s[SN > 0 ? SN : 1];
 };
 
 template <int F, int D>
 struct Decoder {
     using T = Tile<F, D>;
-    static constexpr int ROW = D * kBits<F> / 8;  // bytes of a token's head
+    static constexpr int ROW = T::ROW;
     const DecodeArgs &a;
-    int m, g, b;
+    uint8_t *const lds;  // the wave's part
+    int m, g, b, lane;
     Span sp;
-    // K's and V's first bytes of this lane in page 0, at the first slot of a tile
+    // this head in page 0: K's first bytes of this lane, V's and the scales' first
     const uint8_t *k, *v, *ks, *vs;
     uint32_t page_rows;
     bool bad = false;
 
-    __device__ __forceinline__ Decoder(const DecodeArgs &args, int lane, int seq, int kv_head, int len)
-        : a(args), m(lane & 15), g(lane >> 4), b(seq), sp(span_of(args, len)) {
+    __device__ __forceinline__ Decoder(const DecodeArgs &args, uint8_t *part, int lane, int seq, int kv_head, int len)
+        : a(args), lds(part), m(lane & 15), g(lane >> 4), b(seq), lane(lane), sp(span_of(args, len)) {
         const int ps = 1 << a.c.page_shift;
         page_rows = (uint32_t)a.c.heads << a.c.page_shift;  // a page's bytes fit 32 bits
         const int64_t head = (int64_t)kv_head << a.c.page_shift;
         // K: rows 4g' + i of the first product are tokens 8g' + i, of the second 8g' + 4 + i
-        const int kt = (8 * (m / 4) + m % 4) & (ps - 1), vt = 8 * g & (ps - 1);
+        const int kt = (8 * (m / 4) + m % 4) & (ps - 1);
         k = a.c.k + (head + kt) * ROW + g * T::KB;
-        v = a.c.v + (head + vt) * ROW;
-        ks = a.c.ks + head * (D / 32) + kt;
-        vs = a.c.vs + head * (D / 32) + vt;
+        v = a.c.v + head * ROW;
+        ks = a.c.ks + head * (D / 32);
+        vs = a.c.vs + head * (D / 32);
     }
 
     __device__ __forceinline__ bool sees(int t) const { return (t < sp.len) & ((t >= sp.lo) | (t < a.sinks)); }
@@ -166,7 +176,7 @@ struct Decoder {
             const uint32_t p = table_entry(a.b, b, any ? t >> a.c.page_shift : 0);
             const bool page = p < (uint32_t)a.c.pages;
             bad |= any & !page;
-            r.p[i] = any & page ? p : 0;
+            r.p[i] = (any & page) ? p : 0;
         }
         return r;
     }
@@ -181,41 +191,89 @@ struct Decoder {
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int c = 0; c < T::NC; ++c) load_words<T::KB>(row + 4 * i * ROW + c * 4 * T::KB, r.k[i] + c * T::KW);
-            if constexpr (F != BF16) {
-                const uint8_t *sc = ks + (uint64_t)page * (page_rows * (D / 32)) + slot;
+        }
+        if constexpr (T::STAGED) {
 #pragma unroll
-                for (int c = 0; c < T::NC; ++c) {
-                    const uint8_t *x = sc + (((c * 4 + g) * T::E / 32) << a.c.page_shift);
-                    r.ks[0][c] = x[0];
-                    r.ks[1][c] = x[4];
-                }
+            for (int i = 0; i < T::VN; ++i) {
+                int c = i * 64 + lane;
+                if (T::CHUNKS % 64) c = min(c, T::CHUNKS - 1);  // lanes without a chunk repeat the last
+                const uint32_t t = c / (ROW / 16), piece = c % (ROW / 16), page = t < 16 ? pages.p[0] : pages.p[1];
+                r.v[i] = ld16(v + (uint64_t)page * (page_rows * ROW) + (slot + (t & (uint32_t)(ps - 1))) * ROW + piece * 16);
+            }
+        } else {
+            const uint32_t page = g < 2 ? pages.p[0] : pages.p[1];
+            const uint8_t *row = v + (uint64_t)page * (page_rows * ROW) + (slot + (8 * g & (ps - 1))) * ROW + m * 16;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int n = 0; n < T::N8; ++n) r.v[j * T::N8 + n] = ld16(row + j * ROW + n * 256);
+        }
+#pragma unroll
+        for (int i = 0; i < T::SN; ++i) {
+            int c = i * 64 + lane;
+            if (T::SCALES % 64) c = min(c, T::SCALES - 1);
+            const bool of_v = c >= T::SCALES / 2;
+            const uint32_t blk = (of_v ? c - T::SCALES / 2 : c) / 8, t = 4 * (c % 8), page = t < 16 ? pages.p[0] : pages.p[1];
+            r.s[i] = ld4((of_v ? vs : ks) + (uint64_t)page * (page_rows * (D / 32)) + (blk << a.c.page_shift) + slot + (t & (uint32_t)(ps - 1)));
+        }
+    }
+
+    // What a step works on, read back from LDS.
+    struct Parts {
+        uint32_t v[8][T::VW];
+        u32x2 ks[F == BF16 ? 1 : T::NC], vs[F == BF16 ? 1 : T::NS];
+    };
+    __device__ __forceinline__ void stage(const T &r, Parts &p) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS accesses are in order: no waits
+        if constexpr (T::STAGED) {
+#pragma unroll
+            for (int i = 0; i < T::VN; ++i) {
+                int c = i * 64 + lane;
+                if (T::CHUNKS % 64) c = min(c, T::CHUNKS - 1);
+                *reinterpret_cast<u32x4 *>(lds + c / (ROW / 16) * T::VROW + c % (ROW / 16) * 16) = r.v[i];
             }
         }
-        {
-            const uint32_t page = g < 2 ? pages.p[0] : pages.p[1];
-            const uint8_t *row = v + (uint64_t)page * (page_rows * ROW) + slot * ROW;
-            const uint8_t *r8 = row + m * kBits<F>, *r4 = row + (T::N8 * 128 + m * 4) * kBits<F> / 8,
-                          *r2 = row + (T::N8 * 128 + T::N4 * 64 + m * 2) * kBits<F> / 8;
+#pragma unroll
+        for (int i = 0; i < T::SN; ++i) {
+            int c = i * 64 + lane;
+            if (T::SCALES % 64) c = min(c, T::SCALES - 1);
+            *reinterpret_cast<uint32_t *>(lds + T::SOFF + 4 * c) = r.s[i];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if constexpr (F != BF16) {
+            const uint8_t *sc = lds + T::SOFF + 8 * (m / 4), *sv = lds + T::SOFF + D + 8 * g;
+#pragma unroll
+            for (int c = 0; c < T::NC; ++c) p.ks[c] = ld8(sc + (c * 4 + g) * T::E / 32 * 32);
+#pragma unroll
+            for (int n = 0; n < T::N8; ++n) p.vs[n] = ld8(sv + (n * 4 + m / 4) * 32);
+            if constexpr (T::N4 > 0) p.vs[T::N8] = ld8(sv + (T::N8 * 4 + m / 8) * 32);
+            if constexpr (T::N2 > 0) p.vs[T::N8 + T::N4] = ld8(sv + (T::N8 * 4 + T::N4 * 2) * 32);
+        }
+        if constexpr (T::STAGED) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
+                const uint8_t *row = lds + (8 * g + j) * T::VROW;
 #pragma unroll
-                for (int n = 0; n < T::N8; ++n) load_words<kBits<F>>(r8 + j * ROW + n * 16 * kBits<F>, r.v[j] + n * T::W8);
-                if constexpr (T::N4 > 0) load_words<4 * kBits<F> / 8>(r4 + j * ROW, r.v[j] + T::N8 * T::W8);
-                if constexpr (T::N2 > 0) load_words<2 * kBits<F> / 8>(r2 + j * ROW, r.v[j] + T::N8 * T::W8 + T::N4 * T::W4);
+                for (int n = 0; n < T::N8; ++n) load_words<kBits<F>>(row + (n * 16 + m) * kBits<F>, p.v[j] + n * T::W8);
+                if constexpr (T::N4 > 0)
+                    load_words<4 * kBits<F> / 8>(row + (T::N8 * 128 + m * 4) * kBits<F> / 8, p.v[j] + T::N8 * T::W8);
+                if constexpr (T::N2 > 0)
+                    load_words<2 * kBits<F> / 8>(row + (T::N8 * 128 + T::N4 * 64 + m * 2) * kBits<F> / 8,
+                                                 p.v[j] + T::N8 * T::W8 + T::N4 * T::W4);
             }
-            if constexpr (F != BF16) {
-                const uint8_t *sc = vs + (uint64_t)page * (page_rows * (D / 32)) + slot;
+        } else {
 #pragma unroll
-                for (int n = 0; n < T::N8; ++n) r.vs[n] = ld8(sc + ((n * 4 + m / 4) << a.c.page_shift));
-                if constexpr (T::N4 > 0) r.vs[T::N8] = ld8(sc + ((T::N8 * 4 + m / 8) << a.c.page_shift));
-                if constexpr (T::N2 > 0) r.vs[T::N8 + T::N4] = ld8(sc + ((T::N8 * 4 + T::N4 * 2) << a.c.page_shift));
-            }
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int n = 0; n < T::N8; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p.v[j][4 * n + i] = r.v[j * T::N8 + n][i];
         }
     }
 
     // V of the tokens that the query does not see becomes 0: their weights are
     // 0, and 0 times what lies there must not be NaN.
-    __device__ __forceinline__ void clear_unseen(T &r, int t0) {
+    __device__ __forceinline__ void clear_unseen(Parts &r, int t0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const bool on = sees(t0 + 8 * g + j);
@@ -233,7 +291,7 @@ struct Decoder {
     }
 
     template <int W>
-    __device__ __forceinline__ void add_segment(const T &r, int word, u32x2 vs, bf16x8 p, f32x4 *acc) {
+    __device__ __forceinline__ void add_segment(const Parts &r, int word, u32x2 vs, bf16x8 p, f32x4 *acc) {
         uint32_t c[8][W / 2];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -245,19 +303,22 @@ struct Decoder {
             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(column8<W>(c, t)), p, acc[t], 0, 0, 0);
     }
 
-    __device__ __forceinline__ void step(T &r, int t0, const bf16x8 *q, float &ref, float &sum, f32x4 *acc) {
+    __device__ __forceinline__ void step(const T &tile, int t0, const bf16x8 *q, float &ref, float &sum, f32x4 *acc) {
         // whole tiles that every query head sees need no mask
         const bool whole = t0 + 31 < sp.len && (t0 >= sp.lo || t0 + 31 < a.sinks);
+        Parts r;
+        stage(tile, r);
         f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int c = 0; c < T::NC; ++c) {
-                const float sc = F == BF16 ? 1.0f : e8m0_operand(r.ks[i][F == BF16 ? 0 : c]);
+                const u32x2 sk = r.ks[F == BF16 ? 0 : c];
+                const float sc = F == BF16 ? 1.0f : e8m0_operand((i ? sk.y : sk.x) >> (8 * (m & 3)));
 #pragma unroll
                 for (int e = 0; e < T::E / 8; ++e) {
                     uint32_t o[4];
-                    expand8<F>(r.k[i] + c * T::KW + e * (kBits<F> / 4), sc, o);
+                    expand8<F>(tile.k[i] + c * T::KW + e * (kBits<F> / 4), sc, o);
                     s[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(u32x4{o[0], o[1], o[2], o[3]}),
                                                                    q[c * (T::E / 8) + e], s[i], 0, 0, 0);
                 }
@@ -314,6 +375,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
     constexpr int LD = D + 4;  // padded row: 16 heads' writes of one element land in different banks
     __shared__ float s_acc[4][16][LD];
     __shared__ float s_ref[4][16], s_sum[4][16];
+    __shared__ __align__(16) uint8_t s_tile[4][T::BYTES > 0 ? T::BYTES : 16];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     // ---- this workgroup's piece
@@ -345,7 +407,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
     }
 
     const int kv_head = __builtin_amdgcn_readfirstlane(r / a.tiles);
-    Decoder<F, D> w(a, lane, __builtin_amdgcn_readfirstlane(b), kv_head, __builtin_amdgcn_readfirstlane(len));
+    Decoder<F, D> w(a, s_tile[wave], lane, __builtin_amdgcn_readfirstlane(b), kv_head, __builtin_amdgcn_readfirstlane(len));
     const int h0 = r % a.tiles * 16, heads = min(16, a.group - h0);
     const int hq = kv_head * a.group + h0;  // first query head of the pair
     const int u0 = (int)((int64_t)w.sp.n * piece / pieces), u1 = (int)((int64_t)w.sp.n * (piece + 1) / pieces);
@@ -366,24 +428,37 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
     float ref = kNegInf, sum = 0.0f;
     T cur, nxt;
     const auto token = [&](int u) { return w.unit_token(u) + 32 * wave; };
-    // Two tiles in turn, the next one's loads in flight. The loop's loads are
-    // unconditional, so that the wait for one tile leaves the other's in
-    // flight: the last one or two units come after it.
+    // Two tiles in turn, the next one's loads in flight: issued before the step,
+    // which the scheduling barriers keep (it would move them down to their
+    // use), and unconditional in the loop, so that the wait for one tile leaves
+    // the other's in flight. The last one or two units come after it.
+    const auto load = [&](T &r, int u, typename Decoder<F, D>::Pages p) {
+        w.load(r, token(u), p);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto step = [&](const T &r, int u) {
+        w.step(r, token(u), q, ref, sum, acc);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     if (u0 < u1) {
-        w.load(cur, token(u0), w.pages_of(token(u0)));
+        load(cur, u0, w.pages_of(token(u0)));
         auto next = w.pages_of(token(u0 + 1));
         int u = u0;
         for (; u + 2 < u1; u += 2) {
-            w.load(nxt, token(u + 1), next);
+            load(nxt, u + 1, next);
             next = w.pages_of(token(u + 2));
-            w.step(cur, token(u), q, ref, sum, acc);
-            w.load(cur, token(u + 2), next);
+            step(cur, u);
+            load(cur, u + 2, next);
             next = w.pages_of(token(u + 3));
-            w.step(nxt, token(u + 1), q, ref, sum, acc);
+            step(nxt, u + 1);
         }
-        if (u + 1 < u1) w.load(nxt, token(u + 1), next);
-        w.step(cur, token(u), q, ref, sum, acc);
-        if (u + 1 < u1) w.step(nxt, token(u + 1), q, ref, sum, acc);
+        if (u + 1 < u1) {
+            load(nxt, u + 1, next);
+            step(cur, u);
+            step(nxt, u + 1);
+        } else {
+            step(cur, u);
+        }
     }
     // ---- the four waves' sums meet in LDS
     sum += __shfl_xor(sum, 16);
