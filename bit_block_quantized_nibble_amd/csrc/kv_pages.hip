@@ -5,9 +5,10 @@
 // Each call is a plan by one workgroup (who gets which page: order matters
 // there, so it is prefix sums over the requests and over the pages' reference
 // counts, not atomics) and, where pages move, one wide kernel that copies them
-// in all layers. The plan is bound by latency: its scan reads the counts as
-// 64 pages per wave and step, and ranks come from ballots, with one barrier
-// per pass. The copies are bound by HBM.
+// in all layers and writes the tables that follow from it. The plan is bound
+// by latency: its scan reads the counts as 64 pages per wave and step, eight
+// steps in flight, ranks come from ballots, with one barrier per pass, and what
+// the requests look up stays in LDS where it fits. The copies are bound by HBM.
 //
 // The only atomics are integer sums of reference counts, exchanges of table
 // entries being freed, and minima over request indexes: their order does not
@@ -67,33 +68,46 @@ __device__ __forceinline__ Share share_of(int pages) {
     return {b < pages ? b : pages, b + per < pages ? b + per : pages};
 }
 
+// The counts of 512 pages of a share from p on, eight loads in flight; the first
+// 512 are kept in registers over a plan's passes.
+struct Held {
+    int r[8];
+};
+__device__ __forceinline__ Held hold(const int32_t *refs, Share s, int p) {
+    const int lane = threadIdx.x & 63;
+    Held h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h.r[i] = p + 64 * i + lane < s.end ? refs[p + 64 * i + lane] : 0;
+    return h;
+}
+
 template <typename Fn>
-__device__ __forceinline__ int count_pages(const int32_t *refs, Share s, Fn take) {
+__device__ __forceinline__ int count_pages(const int32_t *refs, Share s, const Held &first, Fn take) {
     const int lane = threadIdx.x & 63;
     int n = 0;
-    for (int p = s.begin + lane; p - lane < s.end; p += 256) {  // four loads in flight
-        int r[4];
+    for (int p = s.begin; p < s.end; p += 512) {
+        const Held h = p == s.begin ? first : hold(refs, s, p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = p + 64 * i < s.end ? refs[p + 64 * i] : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) n += __popcll(__ballot(p + 64 * i < s.end && take(p + 64 * i, r[i])));
+        for (int i = 0; i < 8; ++i) {
+            const int q = p + 64 * i + lane;
+            n += __popcll(__ballot(q < s.end && take(q, h.r[i])));
+        }
     }
     return n;
 }
 
 // emit(page, rank) for the pages taken, in order; `rank` counts from `base`.
 template <typename Fn, typename Out>
-__device__ __forceinline__ void list_pages(const int32_t *refs, Share s, int base, Fn take, Out emit) {
+__device__ __forceinline__ void list_pages(const int32_t *refs, Share s, const Held &first, int base, Fn take, Out emit) {
     const int lane = threadIdx.x & 63;
-    for (int p = s.begin + lane; p - lane < s.end; p += 256) {
-        int r[4];
+    for (int p = s.begin; p < s.end; p += 512) {
+        const Held h = p == s.begin ? first : hold(refs, s, p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = p + 64 * i < s.end ? refs[p + 64 * i] : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool on = p + 64 * i < s.end && take(p + 64 * i, r[i]);
+        for (int i = 0; i < 8; ++i) {
+            const int q = p + 64 * i + lane;
+            const bool on = q < s.end && take(q, h.r[i]);
             const uint64_t votes = __ballot(on);
-            if (on) emit(p + 64 * i, base + __popcll(votes & ((1ull << lane) - 1)));
+            if (on) emit(q, base + __popcll(votes & ((1ull << lane) - 1)));
             base += __popcll(votes);
         }
     }
@@ -119,6 +133,12 @@ struct IsFree {
     __device__ bool operator()(int, int refs) const { return refs == 0; }
 };
 
+// What a plan's requests look up: in LDS up to these sizes, else in the workspace.
+constexpr int kNearSlots = 8192, kNearRequests = 2048, kNearPages = 4096;
+struct Near {
+    int32_t owner[kNearSlots], first[kNearRequests], pages[kNearPages];
+};
+
 // Slots named by requests: owner[slot] = the first request that names it.
 __device__ __forceinline__ void claim(const Pool &p, const Work &w, const int32_t *rows, int count) {
     for (int i = threadIdx.x; i < p.seqs; i += kThreads) w.owner[i] = kNone;
@@ -133,28 +153,30 @@ __device__ __forceinline__ void claim(const Pool &p, const Work &w, const int32_
 // (then first[i] and the pages dst[0..total) are set, with one reference
 // each), else writes the first that cannot to *status.
 template <typename Need>
-__device__ __forceinline__ bool take_pages(const Pool &p, const Work &w, int count, int32_t *status, Need need, int &total_out) {
+__device__ __forceinline__ bool take_pages(const Pool &p, const Work &w, int count, int32_t *status, Need need, int &total_out,
+                                           int32_t *near_pages = nullptr) {
     __shared__ int64_t s_scan[kWaves + 1];
     __shared__ int s_wave[kWaves];
     __shared__ int s_fail;
     const Share sh = share_of(p.pages);
+    const Held held = hold(p.refs, sh, sh.begin);
     int free_pages;
-    const int before_free = wave_prefix(count_pages(p.refs, sh, IsFree{}), s_wave, free_pages);
+    const int before_free = wave_prefix(count_pages(p.refs, sh, held, IsFree{}), s_wave, free_pages);
     if (threadIdx.x == 0) s_fail = kNone;
     const int each = (count + kThreads - 1) / kThreads;
     const int i0 = (int)threadIdx.x * each < count ? (int)threadIdx.x * each : count;
     const int i1 = i0 + each < count ? i0 + each : count;
-    int64_t mine = 0;
+    int64_t mine = 0, own = 0;  // own: the last request's, which is all of them where each is 1
     int fail = kNone;
     for (int i = i0; i < i1; ++i) {
-        const int64_t n = need(i);
-        if (n < 0) fail = i < fail ? i : fail;
-        else mine += n;
+        own = need(i);
+        if (own < 0) fail = i < fail ? i : fail;
+        else mine += own;
     }
     int64_t total;
     int64_t at = block_scan<kThreads>(mine, s_scan, total);  // its barriers also order s_fail
     for (int i = i0; i < i1; ++i) {
-        const int64_t n = need(i);
+        const int64_t n = each == 1 ? own : need(i);
         if (n < 0) continue;
         if (n > 0 && at + n > free_pages) fail = i < fail ? i : fail;
         w.first[i] = (int)(at < kNone ? at : kNone);
@@ -165,9 +187,10 @@ __device__ __forceinline__ bool take_pages(const Pool &p, const Work &w, int cou
     if (threadIdx.x == 0) *status = s_fail == kNone ? -1 : s_fail;
     if (s_fail != kNone) return false;
     const int t = (int)total;  // <= free_pages
-    list_pages(p.refs, sh, before_free, IsFree{}, [&](int page, int rank) {
+    int32_t *const taken = near_pages && t <= kNearPages ? near_pages : w.dst;
+    list_pages(p.refs, sh, held, before_free, IsFree{}, [&](int page, int rank) {
         if (rank < t) {
-            w.dst[rank] = page;
+            taken[rank] = page;
             p.refs[page] = 1;
         }
     });
@@ -178,6 +201,9 @@ __device__ __forceinline__ bool take_pages(const Pool &p, const Work &w, int cou
 
 __global__ __launch_bounds__(kThreads) void k_reserve(Pool p, Work w, int count, const int32_t *rows,
                                                       const int32_t *tokens, int32_t *status) {
+    __shared__ Near s_near;
+    if (p.seqs <= kNearSlots) w.owner = s_near.owner;
+    if (count <= kNearRequests) w.first = s_near.first;
     claim(p, w, rows, count);
     const int ps = 1 << p.page_shift;
     int total = 0;
@@ -190,8 +216,9 @@ __global__ __launch_bounds__(kThreads) void k_reserve(Pool p, Work w, int count,
         const int64_t want = ((int64_t)len + t + ps - 1) >> p.page_shift;
         if (want > p.row) return -1;
         return want - have;
-    }, total);
+    }, total, s_near.pages);
     if (!ok) return;
+    const int32_t *const taken = total <= kNearPages ? s_near.pages : w.dst;
     for (int k = threadIdx.x; k < total; k += kThreads) {  // page k goes to the last request whose first is <= k
         int lo = 0, hi = count - 1;
         while (lo < hi) {
@@ -201,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void k_reserve(Pool p, Work w, int count,
         }
         const int s = rows[lo];
         const int have = (int)(((int64_t)p.lens[s] + ps - 1) >> p.page_shift);
-        p.table[(int64_t)s * p.row + have + (k - w.first[lo])] = w.dst[k];
+        p.table[(int64_t)s * p.row + have + (k - w.first[lo])] = taken[k];
     }
     __syncthreads();  // lens are read above
     for (int i = threadIdx.x; i < count; i += kThreads) p.lens[rows[i]] += tokens[i];
@@ -209,6 +236,8 @@ __global__ __launch_bounds__(kThreads) void k_reserve(Pool p, Work w, int count,
 
 __global__ __launch_bounds__(kThreads) void k_fork(Pool p, Work w, int count, const int32_t *parents,
                                                    const int32_t *children, int32_t *status) {
+    __shared__ int32_t s_owner[kNearSlots];
+    if (p.seqs <= kNearSlots) w.owner = s_owner;
     claim(p, w, children, count);
     const int ps = 1 << p.page_shift;
     int total = 0;
@@ -230,26 +259,23 @@ __global__ __launch_bounds__(kThreads) void k_fork(Pool p, Work w, int count, co
     }
 }
 
-// The children's rows: whole pages shared, the copied page, then none.
-__global__ __launch_bounds__(256) void k_fork_rows(Pool p, Work w, int count, const int32_t *parents,
-                                                   const int32_t *children, const int32_t *status) {
-    if (*status >= 0) return;
-    const int i = blockIdx.y;
-    for (int r = i; r < count; r += gridDim.y) {
+// The entries of the children's rows, spread over the grid: whole pages shared,
+// the copied page, then none.
+__device__ __forceinline__ void fork_rows(const Pool &p, const Work &w, int count, const int32_t *parents, const int32_t *children) {
+    const int64_t n = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)count * p.row; i += n) {
+        const int r = (int)(i / p.row), j = (int)(i % p.row);
         const int a = parents[r], c = children[r], len = w.have[r];
         const int full = len >> p.page_shift;
-        const bool tail = len & ((1 << p.page_shift) - 1);
-        for (int j = blockIdx.x * 256 + threadIdx.x; j < p.row; j += gridDim.x * 256) {
-            int e = -1;
-            if (j < full) {
-                e = p.table[(int64_t)a * p.row + j];
-                if ((uint32_t)e < (uint32_t)p.pages) atomicAdd(&p.refs[e], 1);
-            } else if (j == full && tail) {
-                e = w.dst[w.first[r]];
-            }
-            p.table[(int64_t)c * p.row + j] = e;
+        int e = -1;
+        if (j < full) {
+            e = p.table[(int64_t)a * p.row + j];
+            if ((uint32_t)e < (uint32_t)p.pages) atomicAdd(&p.refs[e], 1);
+        } else if (j == full && (len & ((1 << p.page_shift) - 1))) {
+            e = w.dst[w.first[r]];
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0) p.lens[c] = len;
+        p.table[(int64_t)c * p.row + j] = e;
+        if (j == 0) p.lens[c] = len;
     }
 }
 
@@ -274,21 +300,61 @@ __global__ __launch_bounds__(256) void k_free(Pool p, int count, const int32_t *
     }
 }
 
+// Both in one workgroup, for tables that it passes over faster than two kernels
+// start (2.7 us for 800 entries against 4.8, but 11.5 for 15000 against 9.3):
+// out = in without the pages of the rows named.
+constexpr int64_t kFreeTable = 4096, kFreePages = 4096;
+constexpr int kFreeSlots = 4096;
+__global__ __launch_bounds__(kThreads) void k_copy_free(Pool in, Pool out, int count, const int32_t *rows, int window, int sinks) {
+    __shared__ uint32_t s_named[kFreeSlots / 32];
+    for (int i = threadIdx.x; i < (in.seqs + 31) / 32; i += kThreads) s_named[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < count; i += kThreads)
+        if ((uint32_t)rows[i] < (uint32_t)in.seqs) atomicOr(&s_named[rows[i] / 32], 1u << (rows[i] % 32));
+    for (int q = threadIdx.x; q < in.pages; q += kThreads) out.refs[q] = in.refs[q];
+    __syncthreads();
+    const int first = (int)(((int64_t)sinks + (1 << in.page_shift) - 1) >> in.page_shift < in.row
+                                ? ((int64_t)sinks + (1 << in.page_shift) - 1) >> in.page_shift
+                                : in.row);
+    const int entries = in.seqs * in.row;
+    for (int i0 = threadIdx.x; i0 < entries; i0 += 4 * kThreads) {
+        int e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = i0 + k * kThreads < entries ? in.table[i0 + k * kThreads] : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * kThreads;
+            if (i >= entries) break;
+            const int s = i / in.row, j = i % in.row;
+            bool gone = s_named[s / 32] >> (s % 32) & 1;
+            if (gone && window > 0) {
+                const int64_t end = (int64_t)in.lens[s] - window;  // tokens before it are out of the window
+                gone = j >= first && j < (end > 0 ? end >> in.page_shift : 0);
+            }
+            if (gone && (uint32_t)e[k] < (uint32_t)in.pages) atomicSub(&out.refs[e[k]], 1);
+            out.table[i] = gone ? -1 : e[k];
+        }
+    }
+    for (int s = threadIdx.x; s < in.seqs; s += kThreads)
+        out.lens[s] = window <= 0 && (s_named[s / 32] >> (s % 32) & 1) ? 0 : in.lens[s];
+}
+
 __global__ __launch_bounds__(kThreads) void k_compact(Pool p, Work w, int32_t *live_out) {
     __shared__ int s_wave[kWaves];
     const Share sh = share_of(p.pages);
     int live, low;
     const auto used = [](int, int r) { return r > 0; };
-    const int before = wave_prefix(count_pages(p.refs, sh, used), s_wave, live);
-    wave_prefix(count_pages(p.refs, sh, [&](int q, int r) { return r > 0 && q < live; }), s_wave, low);
+    const Held held = hold(p.refs, sh, sh.begin);
+    const int before = wave_prefix(count_pages(p.refs, sh, held, used), s_wave, live);
+    wave_prefix(count_pages(p.refs, sh, held, [&](int q, int r) { return r > 0 && q < live; }), s_wave, low);
     const int moves = live - low;
-    for (int q = threadIdx.x; q < p.pages; q += kThreads) w.map[q] = q;
     // pages in use, ranked: the ones at or beyond `live` come after the `low` ones below
-    list_pages(p.refs, sh, before, used, [&](int q, int rank) {
+    list_pages(p.refs, sh, held, before, used, [&](int q, int rank) {
         if (q >= live) w.src[rank - low] = q;
     });
-    list_pages(p.refs, sh, sh.begin - before, [](int, int r) { return r <= 0; }, [&](int q, int rank) {
+    list_pages(p.refs, sh, held, sh.begin - before, [](int, int r) { return r <= 0; }, [&](int q, int rank) {
         if (q < live) w.dst[rank] = q;
+        else w.map[q] = q;  // a broken table may name it: the entry stays
     });
     if (threadIdx.x == 0) {
         *w.moves = moves;
@@ -312,13 +378,20 @@ struct MoveArgs {
 };
 
 // Copies pages src[i] -> dst[i] in every layer (the two lists have no page in
-// common), and, given a map, rewrites the table by it.
-__global__ __launch_bounds__(256) void k_move(MoveArgs m, Pool p, Work w, bool remap) {
-    if (remap) {
+// common), and writes the table: the forked rows, or, after packing, the new
+// places of the pages at and beyond *word, the number of pages in use.
+template <bool FORK>
+__global__ __launch_bounds__(256) void k_move(MoveArgs m, Pool p, Work w, int count, const int32_t *parents,
+                                              const int32_t *children, const int32_t *word) {
+    if constexpr (FORK) {
+        if (*word >= 0) return;  // a request could not be met
+        fork_rows(p, w, count, parents, children);
+    } else {
+        const int live = *word;
         const int64_t n = (int64_t)gridDim.x * 256;
         for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)p.seqs * p.row; i += n) {
             const int e = p.table[i];
-            if ((uint32_t)e < (uint32_t)p.pages) p.table[i] = w.map[e];
+            if (e >= live && e < p.pages) p.table[i] = w.map[e];
         }
     }
     const int64_t units = (int64_t)*w.moves * m.layers * m.chunk_sum;
@@ -393,15 +466,19 @@ hipError_t launch_kv_fork(const qbn_kv_cache &c, const qbn_kv_pool &in, const qb
     const Work w = work_of(ws, out.seqs, count, out.pages);
     k_fork<<<1, kThreads, 0, s>>>(p, w, (int)count, parents, children, status);
     if (count > 0 && p.row > 0) {
-        k_fork_rows<<<dim3(row_blocks(p.row), at_most(count, 4096)), 256, 0, s>>>(p, w, (int)count, parents, children, status);
         const MoveArgs m = move_args(c);
-        k_move<<<at_most(count * m.layers * m.chunk_sum, 4096), 256, 0, s>>>(m, p, w, false);
+        const int64_t copies = count * m.layers * m.chunk_sum, entries = (count * p.row + 255) / 256;
+        k_move<true><<<at_most(copies > entries ? copies : entries, 4096), 256, 0, s>>>(m, p, w, (int)count, parents, children, status);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_kv_free(const qbn_kv_pool &in, const qbn_kv_pool &out, int64_t count, const int32_t *rows,
                           int window, int sinks, hipStream_t s) {
+    if (in.table != out.table && in.seqs * in.row <= kFreeTable && in.pages <= kFreePages && in.seqs <= kFreeSlots && count <= kFreeSlots) {
+        k_copy_free<<<1, kThreads, 0, s>>>(pool_of(in), pool_of(out), (int)count, rows, window, sinks);
+        return hipGetLastError();
+    }
     copy_pool(in, out, s);
     if (count > 0)
         k_free<<<dim3(out.row > 0 ? row_blocks(out.row) : 1, at_most(count, 4096)), 256, 0, s>>>(pool_of(out), (int)count, rows, window, sinks);
@@ -415,7 +492,7 @@ hipError_t launch_kv_compact(const qbn_kv_cache &c, const qbn_kv_pool &in, const
     const Work w = work_of(ws, out.seqs, 0, out.pages);
     k_compact<<<1, kThreads, 0, s>>>(p, w, live);
     const MoveArgs m = move_args(c);
-    k_move<<<4096, 256, 0, s>>>(m, p, w, true);
+    k_move<false><<<4096, 256, 0, s>>>(m, p, w, 0, nullptr, nullptr, live);
     return hipGetLastError();
 }
 

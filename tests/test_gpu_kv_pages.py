@@ -114,6 +114,68 @@ def test_reserve_many(pages, seqs):
     same(pool, ref)
 
 
+def test_sizes_beyond_the_near_lookups():
+    """More slots, requests, pages and entries than fit the plans' LDS, with a
+    failing request at the end of one call."""
+    rng = np.random.default_rng(41)
+    seqs, row, ps, pages = 9001, 9, 16, 60000
+    table = np.full((seqs, row), -1, np.int32)
+    refs = (rng.random(pages) < 0.1).astype(np.int32)
+    pool = qbn.KVPool(torch.from_numpy(table).to(DEV), ints(np.zeros(seqs)), ints(refs), ps)
+    ref = R.RefPool(table, np.zeros(seqs, np.int32), refs, ps)
+    rows, tokens = rng.permutation(seqs)[:3000], rng.integers(0, row * ps + 1, 3000)
+    say("reserve", seqs, pages)
+    st = qbn.kv_reserve(pool, ints(rows), ints(tokens))
+    assert int(st) == ref.reserve(rows.tolist(), tokens.tolist()) == -1
+    same(pool, ref)
+    other = rng.permutation(seqs)[:2500]
+    st = qbn.kv_reserve(pool, ints(list(other) + [seqs]), ints([0] * 2501))
+    assert int(st) == ref.reserve(list(other) + [seqs], [0] * 2501) == 2500
+    same(pool, ref)
+    gone = rng.permutation(seqs)[:4000]
+    after = qbn.KVPool.like(pool)
+    say("free", len(gone))
+    qbn.kv_free(pool, ints(gone), out=after)
+    ref.release(gone.tolist())
+    same(after, ref)
+    c = qbn.KVCache.empty("mxfp4", 1, pages, 1, ps, 64, device=DEV)
+    kids = [int(b) for b in range(seqs) if ref.lens[b] == 0][:2500]
+    parents = [int(b) for b in rng.choice([b for b in range(seqs) if ref.lens[b] > 0], 2500)]
+    say("fork", len(kids))
+    st = qbn.kv_fork(c, after, ints(parents), ints(kids))
+    assert int(st) == ref.fork(parents, kids) == -1
+    same(after, ref)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (20, 5), (100, 33)])
+def test_free_into_other_tables(window, sinks):
+    """out = in without the pages given back, in as it was."""
+    rng = np.random.default_rng(window + sinks + 1)
+    c, pool, ref = make(rng, pages=60, row=20, lens=(300, 16, 3, 0, 97, 320))
+    pool.table[3, 2], ref.table[3, 2] = 77, 77  # no page: gone without a count
+    old = [t.clone() for t in (pool.table, pool.lens, pool.refs)]
+    out = qbn.KVPool.like(pool)
+    rows = [0, 1, 2, 3, 5, 5, 7, -2]
+    qbn.kv_free(pool, ints(rows), window=window, sinks=sinks, out=out)
+    ref.release(rows, window, sinks)
+    same(out, ref)
+    for x, y in zip(old, (pool.table, pool.lens, pool.refs)):
+        assert torch.equal(x, y)
+
+
+def test_compact_keeps_entries_that_name_free_pages():
+    rng = np.random.default_rng(44)
+    c, pool, ref = make(rng)
+    free = [p for p in range(40) if ref.refs[p] == 0]
+    pool.table[5, 0], pool.table[5, 1] = free[-1], free[0]
+    ref.table[5, 0], ref.table[5, 1] = free[-1], free[0]
+    before = payload(c)
+    qbn.kv_compact(c, pool)
+    ref.compact()
+    same(pool, ref)
+    same_payload(c, before, ref.moves)
+
+
 @pytest.mark.parametrize("rows,tokens", [
     ([0, 7], [1, 1]),           # no such slot
     ([0, -1], [1, 1]),
