@@ -396,9 +396,9 @@ __global__ __launch_bounds__(256) void k_move(MoveArgs m, Pool p, Work w, int co
     }
     const int64_t units = (int64_t)*w.moves * m.layers * m.chunk_sum;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        int c = (int)(u % m.chunk_sum);
-        const int64_t pl = u / m.chunk_sum;
-        const int layer = (int)(pl % m.layers), i = (int)(pl / m.layers);
+        const int64_t pl = div_i64(u, m.chunk_sum);
+        int c = (int)(u - pl * m.chunk_sum);
+        const int i = (int)div_i64(pl, m.layers), layer = (int)(pl - (int64_t)i * m.layers);
         int b = 0;
         while (c >= m.chunks[b]) c -= m.chunks[b++];
         const int64_t bytes = m.page_bytes[b], o = (int64_t)c * 16384 + threadIdx.x * 16;
@@ -407,10 +407,10 @@ __global__ __launch_bounds__(256) void k_move(MoveArgs m, Pool p, Work w, int co
         u32x4 t[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (o + k * 4096 < bytes) t[k] = ld16(src + k * 4096);
+            if (o + k * 4096 < bytes) t[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(src + k * 4096));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (o + k * 4096 < bytes) *reinterpret_cast<u32x4 *>(dst + k * 4096) = t[k];
+            if (o + k * 4096 < bytes) __builtin_nontemporal_store(t[k], reinterpret_cast<u32x4 *>(dst + k * 4096));
     }
 }
 
