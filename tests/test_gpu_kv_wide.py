@@ -170,3 +170,46 @@ def test_side_stream_and_given_buffers():
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     assert a is out and b is lse and torch.equal(out, want) and torch.equal(lse, lse0)
+
+
+def test_decode_calls_on_two_streams_at_once():
+    """Calls that overlap, each with a workspace of its own, give the bits of calls alone."""
+    rng = np.random.default_rng(71)
+    lens, ps, dim = [6000, 4000, 300], 64, 64
+    c, table = setup("mxfp4", dim, ps, 2, lens, rng)
+    t, n = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    qs = [vectors(rng, 3, 8, dim).to(DEV) for _ in range(2)]
+    want = [qbn.kv_attention_decode(c, q, t, n) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = [[], []]
+    for rep in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(qbn.kv_attention_decode(c, qs[i], t, n))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_split_decode_in_a_graph_beside_eager_calls():
+    rng = np.random.default_rng(72)
+    lens, ps, dim = [6000, 900], 64, 128
+    c, table = setup("mxfp8", dim, ps, 2, lens, rng)
+    t, n = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q = vectors(rng, 2, 8, dim).to(DEV)
+    qbn.kv_attention_decode(c, q, t, n)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = qbn.kv_attention_decode(c, q, t, n)
+    for rep in range(4):
+        q.copy_(vectors(rng, 2, 8, dim))
+        want = qbn.kv_attention_decode(c, q, t, n)
+        torch.cuda.synchronize()
+        say("graph replay", rep)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    del g
