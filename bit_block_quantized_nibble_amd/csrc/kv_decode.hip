@@ -96,6 +96,7 @@ __device__ __forceinline__ uint32_t pieces_of(const DecodeArgs &a, int len, uint
 
 struct Plan {
     int first;     // lengths of sequences 0 .. 63, one per lane
+    Chunk pieces;  // of those
     uint32_t per;  // units of a piece at most
 };
 __device__ __forceinline__ Plan plan_units(const DecodeArgs &a) {
@@ -105,6 +106,17 @@ __device__ __forceinline__ Plan plan_units(const DecodeArgs &a) {
     for (int s = 64; s < a.b.seqs; s += 64) total += scan_of(span_of(a, length_at(a, s)).n).all;
     const int64_t per = div_i64(total * a.rows + a.blocks - 1, a.blocks);
     p.per = (uint32_t)(per < 1 ? 1 : per < (1 << 24) ? per : 1 << 24);
+    // Rounded up pair by pair, that may be a few pieces more than run at once,
+    // and those would double the time: longer pieces, until all fit.
+    p.pieces = scan_of(pieces_of(a, p.first, p.per));
+    for (int i = 0; i < 8 && (int64_t)a.b.seqs * a.rows <= a.blocks; ++i) {
+        int64_t pieces = p.pieces.all;
+        for (int s = 64; s < a.b.seqs; s += 64) pieces += scan_of(pieces_of(a, length_at(a, s), p.per)).all;
+        pieces *= a.rows;  // fewer than 2^31
+        if (pieces <= a.blocks) break;
+        p.per = max(p.per + 1, (uint32_t)div_i64(p.per * pieces + a.blocks - 1, a.blocks));
+        p.pieces = scan_of(pieces_of(a, p.first, p.per));
+    }
     return p;
 }
 
@@ -387,7 +399,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
     } else {
         const Plan p = plan_units(a);
         int lens = p.first;
-        Chunk c = scan_of(pieces_of(a, lens, p.per));
+        Chunk c = p.pieces;
         int64_t before = 0;
         int s0 = 0;
         while (blockIdx.x >= (before + c.all) * a.rows) {
@@ -536,7 +548,7 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a) {
     // pieces before this sequence, and its own
     const Plan p = plan_units(a);
     int64_t before = 0;
-    Chunk c = scan_of(pieces_of(a, p.first, p.per));
+    Chunk c = p.pieces;
     for (int s = 64; s <= b; s += 64) {
         before += c.all;
         c = scan_of(pieces_of(a, length_at(a, s), p.per));
@@ -619,7 +631,10 @@ Cut plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int windo
         const int64_t seen = (int64_t)window / kUnit + 2 + ((int64_t)sinks + kUnit - 1) / kUnit;
         if (seen < p.units) p.units = seen;
     }
-    p.blocks = p.units <= 2 ? 0 : 512;
+    // Up to two units a pair: one workgroup each. More: as many pieces as run at
+    // once (two workgroups of 256 threads on a compute unit, one where the
+    // head's sums take more than 256 registers).
+    p.blocks = p.units <= 2 ? 0 : c.head_dim <= 128 ? 512 : 256;
     return p;
 }
 
