@@ -93,8 +93,8 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
         const int64_t head = (int64_t)page * a.heads + h;
         uint8_t *dst = (is_v ? a.v : a.k) + ((head * ps + slot) * a.dim + d) * kBits<F> / 8;
         if constexpr (F == BF16) {
-            *reinterpret_cast<u32x4 *>(dst) = u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                    pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+            *reinterpret_cast<u32x4 *>(dst) = u32x4{pack2(x[0], x[1]), pack2(x[2], x[3]),
+                                                    pack2(x[4], x[5]), pack2(x[6], x[7])};
         } else {
             uint32_t top = 0;  // magnitudes as bit patterns order like the values
 #pragma unroll

@@ -374,7 +374,7 @@ struct Decoder {
             const float p0 = exp2_fast(__builtin_fmaf(x[j], a.scale, -base));
             const float p1 = exp2_fast(__builtin_fmaf(x[j + 1], a.scale, -base));
             sum += p0 + p1;
-            p[j / 2] = pack_bf16x2(p0, p1);
+            p[j / 2] = pack2(p0, p1);
         }
         const bf16x8 pb = as_bf16x8(p);
 #pragma unroll
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
             const float inv = total == 0.0f ? 0.0f : 1.0f / total;
             const int64_t row = (int64_t)w.b * a.rows / a.tiles * a.group + hq + h;
             *reinterpret_cast<u32x2 *>(a.out + row * D + d) =
-                u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+                u32x2{pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
             if (d == 0 && a.lse) a.lse[row] = total == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(total)) * kLn2;
         } else {
             *reinterpret_cast<f32x4 *>(part + h * D + d) = o;
@@ -621,7 +621,7 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a) {
         sum += s_sum[s0 + k];
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    *reinterpret_cast<u32x2 *>(a.out + row * D + d) = u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<u32x2 *>(a.out + row * D + d) = u32x2{pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
     if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 

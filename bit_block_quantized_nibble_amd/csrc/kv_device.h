@@ -135,6 +135,12 @@ __device__ __forceinline__ u32x4 column8(const uint32_t (&c)[8][W / 2], int t) {
                  __builtin_amdgcn_perm(c[7][t / 2], c[6][t / 2], sel)};
 }
 
+// Two binary32 values rounded to bfloat16 (nearest even), low half first. As a
+// vector conversion this is one instruction; two scalar ones put together are four.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 // v_exp_f32: 2^x within one unit in the last place, 2^-inf = 0. Results below

@@ -296,7 +296,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         if (k >= 2) {
             const float y = pow[k % 2][0], z = pow[k % 2][1];
             sum = here(sum + (y + z));
-            w.p[(k - 2) / 4][(k - 2) % 4] = here(pack_bf16x2(y, z));
+            w.p[(k - 2) / 4][(k - 2) % 4] = here(pack2(y, z));
         }
         if (k < 16) {
 #pragma unroll
@@ -453,8 +453,8 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<u32x2 *>(a.out + row * D + 32 * t + 8 * i + 4 * half) =
-                    u32x2{pack_bf16x2(acc[t][4 * i] * inv, acc[t][4 * i + 1] * inv),
-                          pack_bf16x2(acc[t][4 * i + 2] * inv, acc[t][4 * i + 3] * inv)};
+                    u32x2{pack2(acc[t][4 * i] * inv, acc[t][4 * i + 1] * inv),
+                          pack2(acc[t][4 * i + 2] * inv, acc[t][4 * i + 3] * inv)};
         if (half == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (ref + __builtin_amdgcn_logf(sum)) * kLn2;
     } else if (mine) {
 #pragma unroll
@@ -535,7 +535,7 @@ __global__ __launch_bounds__(256) void k_prefill_join(PrefillArgs a, int64_t tot
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    *reinterpret_cast<u32x2 *>(a.out + row * D + d) = u32x2{pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<u32x2 *>(a.out + row * D + d) = u32x2{pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
     if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 

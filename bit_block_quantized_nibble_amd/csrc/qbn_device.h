@@ -71,10 +71,8 @@ __device__ __forceinline__ uint16_t bf16_bits_rne(float f) {
     return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
-// Two at once: as a vector conversion this is one instruction, as two scalar
-// ones put together it is four.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+    return (uint32_t)bf16_bits_rne(lo) | ((uint32_t)bf16_bits_rne(hi) << 16);
 }
 
 // Reinterpret a 32-bit value as two bfloat16 / two fp16 (low half first).
