@@ -66,9 +66,14 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     const int64_t units = (int64_t)a.b.tokens * 2 * a.chunks;
     const int ps = 1 << a.page_shift, width = a.heads * a.dim;
     for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < units; u += waves) {
-        const int token = (int)(u / (2 * a.chunks)), rest = (int)(u % (2 * a.chunks));
+        const int token = (int)div_i64(u, 2 * a.chunks), rest = (int)(u - (int64_t)token * 2 * a.chunks);
         const bool is_v = rest >= a.chunks;
         const int e0 = (is_v ? rest - a.chunks : rest) * 512 + lane * 8;
+        // the elements do not wait for the token's place
+        const int at = min(e0, width - 8), h = at / a.dim, d = at - h * a.dim;
+        const T *src = is_v ? (const T *)a.sv + token * a.vt + h * a.vh + d : (const T *)a.sk + token * a.kt + h * a.kh + d;
+        float x[8];
+        load8<T>(src, x);
         // the sequence: how many of cu[1..seqs] are <= token
         int b = token, left = 1;
         if (a.b.cu) {
@@ -86,10 +91,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
         if (pos < 0 || (pos >> a.page_shift) >= a.b.row) continue;
         const int page = a.b.table[(int64_t)b * a.b.row_stride + (pos >> a.page_shift)];
         if ((uint32_t)page >= (uint32_t)a.pages || e0 >= width) continue;
-        const int slot = (int)pos & (ps - 1), h = e0 / a.dim, d = e0 - h * a.dim;
-        const T *src = is_v ? (const T *)a.sv + token * a.vt + h * a.vh + d : (const T *)a.sk + token * a.kt + h * a.kh + d;
-        float x[8];
-        load8<T>(src, x);
+        const int slot = (int)pos & (ps - 1);
         const int64_t head = (int64_t)page * a.heads + h;
         uint8_t *dst = (is_v ? a.v : a.k) + ((head * ps + slot) * a.dim + d) * kBits<F> / 8;
         if constexpr (F == BF16) {

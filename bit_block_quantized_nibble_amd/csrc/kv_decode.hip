@@ -60,6 +60,7 @@ struct DecodeArgs {
     __bf16 *out;
     float *lse;
     float *parts;  // pieces: [16][D] sums, then [16] maxima and [16] sums of weights
+    int2 *found;   // per pair: its first piece, how many there are
     float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
     uint32_t q_keep, q_flip;
     int group, tiles, rows;  // query heads per key-value head, 16-row tiles of them, pairs per sequence
@@ -100,8 +101,10 @@ __device__ __forceinline__ int length_at(const DecodeArgs &a, int s0) {  // of t
     const int s = s0 + (threadIdx.x & 63);
     return s < a.b.seqs ? a.b.lens[s] : 0;
 }
-__device__ __forceinline__ uint32_t pieces_of(const DecodeArgs &a, int len, uint32_t per) {
-    return ((uint32_t)span_of(a, len).n + per - 1) / per;
+__device__ __forceinline__ uint32_t pieces_at(const DecodeArgs &a, int s0, int len, uint32_t per) {  // of this lane's sequence
+    if (s0 + (int)(threadIdx.x & 63) >= a.b.seqs) return 0;
+    const uint32_t n = (uint32_t)span_of(a, len).n;
+    return n == 0 ? 1 : (n + per - 1) / per;  // a sequence without tokens has outputs to be written, too
 }
 
 struct Plan {
@@ -118,14 +121,14 @@ __device__ __forceinline__ Plan plan_units(const DecodeArgs &a) {
     p.per = (uint32_t)(per < 1 ? 1 : per < (1 << 24) ? per : 1 << 24);
     // Rounded up pair by pair, that may be a few pieces more than run at once,
     // and those would double the time: longer pieces, until all fit.
-    p.pieces = scan_of(pieces_of(a, p.first, p.per));
+    p.pieces = scan_of(pieces_at(a, 0, p.first, p.per));
     for (int i = 0; i < 8 && (int64_t)a.b.seqs * a.rows <= a.blocks; ++i) {
         int64_t pieces = p.pieces.all;
-        for (int s = 64; s < a.b.seqs; s += 64) pieces += scan_of(pieces_of(a, length_at(a, s), p.per)).all;
+        for (int s = 64; s < a.b.seqs; s += 64) pieces += scan_of(pieces_at(a, s, length_at(a, s), p.per)).all;
         pieces *= a.rows;  // fewer than 2^31
         if (pieces <= a.blocks) break;
         p.per = max(p.per + 1, (uint32_t)div_i64(p.per * pieces + a.blocks - 1, a.blocks));
-        p.pieces = scan_of(pieces_of(a, p.first, p.per));
+        p.pieces = scan_of(pieces_at(a, 0, p.first, p.per));
     }
     return p;
 }
@@ -417,7 +420,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
             s0 += 64;
             if (s0 >= a.b.seqs) return;  // more workgroups than pieces
             lens = length_at(a, s0);
-            c = scan_of(pieces_of(a, lens, p.per));
+            c = scan_of(pieces_at(a, s0, lens, p.per));
         }
         const int at = __builtin_ctzll(__ballot(blockIdx.x < (before + c.upto) * a.rows));
         b = s0 + at;
@@ -426,6 +429,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
         const uint32_t rest = (uint32_t)(blockIdx.x - (before + __builtin_amdgcn_readlane(c.upto, at) - pieces) * a.rows);
         r = rest / pieces;
         piece = rest % pieces;
+        if (piece == 0 && tid == 0) a.found[(int64_t)b * a.rows + r] = int2{(int)blockIdx.x, pieces};
     }
 
     const int kv_head = __builtin_amdgcn_readfirstlane(r / a.tiles);
@@ -555,25 +559,11 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a) {
     if (row >= (int64_t)a.b.seqs * q_heads) return;                // W == 1 only: no barrier below
     const int b = (int)(row / q_heads), hq = (int)(row % q_heads);
     const int kv_head = hq / a.group, hg = hq % a.group;
-    // pieces before this sequence, and its own
-    const Plan p = plan_units(a);
-    int64_t before = 0;
-    Chunk c = p.pieces;
-    for (int s = 64; s <= b; s += 64) {
-        before += c.all;
-        c = scan_of(pieces_of(a, length_at(a, s), p.per));
-    }
-    const int count = __builtin_amdgcn_readlane(c.n, b & 63);
-    before += __builtin_amdgcn_readlane(c.upto, b & 63) - count;
-    if (count == 0) {
-        const float none = span_of(a, length_of(a.b, b)).bad ? __builtin_nanf("") : 0.0f;
-        for (int d = lane; d < D; d += 64) a.out[row * D + d] = (__bf16)none;
-        if (lane == 0 && a.lse) a.lse[row] = none == 0.0f ? kNegInf : none;
-        return;
-    }
-    if (count == 1) return;  // written by its workgroup
     const int r = kv_head * a.tiles + hg / 16, h = hg % 16;
-    const float *part = a.parts + (before * a.rows + (int64_t)r * count) * SLOT;
+    const int2 found = a.found[(int64_t)b * a.rows + r];
+    const int count = found.y;
+    if (count == 1) return;  // written by its workgroup
+    const float *part = a.parts + (int64_t)found.x * SLOT;
     const int sub = wave % W * PW + lane / L, d = lane % L * 4;
     const bool on = lane < PW * L;
     const auto at = [&](int k) { return part + (int64_t)(k * SUBS + sub < count ? k * SUBS + sub : 0) * SLOT; };
@@ -681,7 +671,7 @@ hipError_t launch(const DecodeArgs &a, int64_t grid, hipStream_t s) {
 
 int64_t kv_decode_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     const Cut p = plan_of(c, b, q_heads, window, sinks);
-    return p.blocks ? most_pieces(p) * (16 * (int64_t)c.head_dim + 32) * 4 : 0;
+    return p.blocks ? most_pieces(p) * (16 * (int64_t)c.head_dim + 32) * 4 + p.pairs * 8 : 0;
 }
 
 hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, int q_heads, const KvRows &q,
@@ -698,6 +688,7 @@ hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_b
     a.qt = q.token_stride, a.qh = q.head_stride;
     a.out = (__bf16 *)out, a.lse = lse;
     a.parts = p.blocks ? (float *)ws : nullptr;
+    a.found = p.blocks ? (int2 *)(a.parts + most_pieces(p) * (16 * c.head_dim + 32)) : nullptr;
     a.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
     a.q_keep = scale == 0.0f ? 0u : ~0u;
     a.q_flip = scale < 0.0f ? 0x80008000u : 0u;
