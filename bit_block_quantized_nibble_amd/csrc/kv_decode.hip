@@ -28,20 +28,21 @@
 // about `blocks` pieces come out of all pairs, whatever the lengths. The
 // pieces of a pair are alike; each workgroup finds its own by a scan of the
 // lengths. A pair of one piece is written at once; the pieces of the others go
-// through the workspace and a second kernel joins them in order. (Pieces that
+// through the workspace, where the first of them notes which they are, and a
+// second kernel joins them in order. (Pieces that
 // run over the end of a pair into the next one would be more even, but the
 // workgroups that hold an end then pass twice through the chain of length,
 // page table, first tile and output, and that chain is most of a short call.)
 //
 // Measured (kernel and join, one layer): 32 sequences of up to 4096 tokens, 8
-// heads of 128, MXFP8 (100 MB): 22.6 + 4.8 us, 4.4 TB/s in the first; two of
-// up to 131072 tokens, MXFP4 (179 MB): 36.4 + 5.3 us, 4.9 TB/s, what a copy of
-// 2 GiB reaches; 64 with a window of 4096 and one head of 64, MXFP4 (15 MB):
-// 10.4 + 4.1 us, of which 4 are the chain of launch, lengths, table, first tile
+// heads of 128, MXFP8 (100 MB): 23.0 + 3.9 us, 4.3 TB/s in the first; two of
+// up to 131072 tokens, MXFP4 (179 MB): 37.0 + 4.8 us, 4.8 TB/s, nearly what
+// a copy of 2 GiB reaches (4.95); 64 with a window of 4096 and one head of 64,
+// MXFP4 (15 MB): 10.7 + 4.2 us, of which 4 are the chain of launch, lengths, table, first tile
 // and output, and the rest is instruction issue. Tried and slower: three or four
 // tiles in flight (batch 28.9 -> 32.6 us), 1024 pieces instead of 512 (long
 // 37.4 -> 39.7), and the join inside this kernel by the workgroup that
-// finishes last (long 41.4 -> 46.4, window 12.8 -> 11.8).
+// finishes last (long 41.4 -> 46.4, though window 12.8 -> 11.8).
 #include "kv_device.h"
 #include "kv_launch.h"
 

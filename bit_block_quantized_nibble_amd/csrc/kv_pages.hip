@@ -10,8 +10,8 @@
 // steps in flight, ranks come from ballots, with one barrier per pass, and what
 // the requests look up stays in LDS where it fits. The copies are bound by HBM.
 //
-// Measured: a turn of 36 sequences in 309 pages (free, fork, reserve, compact) 29.6
-// us of launches; of 120 sequences in 5238 pages 158 us, of which packing moves
+// Measured: a turn of 36 sequences in 309 pages (free, fork, reserve, compact) 30
+// us of launches; of 120 sequences in 5238 pages 160 us, of which packing moves
 // 691 MB in 132 us (5.2 TB/s; a copy of 2 GiB reaches 4.95).
 //
 // The only atomics are integer sums of reference counts, exchanges of table

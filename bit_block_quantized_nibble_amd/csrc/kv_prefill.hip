@@ -21,12 +21,13 @@
 // tile of 32 rows and 64 tokens (head_dim 128) is 32 products of 33.5 cycles
 // and about 200 vector instructions of 4.5, two waves share a SIMD, and under
 // this load the clock is near 2.0 GHz. Measured: a prompt of 4096 tokens, 32
-// query and 8 key-value heads of 128, bf16 cache: 141 us, 970 TFLOP/s of
+// query and 8 key-value heads of 128, bf16 cache: 143 us, 960 TFLOP/s of
 // causal products (the library's product of 8192^3 reaches 1327); 8192 new
-// tokens of 16384 with a window of 2048, MXFP4: 304 us, 910 TFLOP/s. Tried and
+// tokens of 16384 with a window of 2048, MXFP4: 306 us, 900 TFLOP/s. Tried and
 // slower or equal: 64 rows a wave (199 and 392 us: copies to and from the
 // accumulation registers), raised wave priority in either product, operands
-// read 3 or 6 steps ahead, the barrier inside the second product.
+// read 3 or 6 steps ahead, the barrier inside the second product, four of the
+// eight waves half a turn behind the others (148 and 317 us).
 #include "kv_device.h"
 #include "kv_launch.h"
 
