@@ -48,6 +48,10 @@ __device__ __forceinline__ int length_of(const Batch &b, int seq) {
     typedef const int32_t __attribute__((address_space(4))) *Const;
     return ((Const)(uintptr_t)b.lens)[seq];
 }
+__device__ __forceinline__ int start_of(const Batch &b, int seq) {
+    typedef const int32_t __attribute__((address_space(4))) *Const;
+    return ((Const)(uintptr_t)b.cu)[seq];
+}
 
 // Eight consecutive elements (4, 8 or 16 bytes in w) -> bf16 pairs, exact: an
 // E2M1 or E4M3FN value has at most 4 significant bits.

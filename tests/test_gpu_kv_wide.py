@@ -120,6 +120,55 @@ def test_scales(fmt, scale):
     check(c, out, lse, q[:2], table, lens, [1, 1], 0, 0, scale=s)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("ragged", [True, False])
+def test_append_many_tokens(fmt, dtype, ragged):
+    """Several tokens a wave: groups of tokens that cross sequences and pages, empty
+    sequences, tokens without a page, before position 0, beyond the row and beyond
+    cu. Whatever is not a token's place keeps its bytes."""
+    rng = np.random.default_rng(90 + ragged)
+    heads, dim, ps, row = 61, 96, 16, 12
+    if ragged:
+        news = [1, 0, 2, 131, 0, 0, 1, 1, 61, 70, 5, 96, 3]
+        lens = [n + int(rng.integers(0, 40)) for n in news]
+        lens[8] = 23            # 38 of its 61 tokens stand before position 0
+        lens[9] = ps * row + 9  # the last 9 stand beyond the row
+        cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        tokens = int(cu[-1]) + 6  # the last 6 belong to no sequence
+    else:
+        tokens = 413
+        news, cu = [1] * tokens, None
+        lens = [int(n) for n in rng.integers(0, 2 * ps + 1, tokens)]
+    table = R.torch_table([min(n, ps * row) for n in lens], ps, row, sum(-(-n // ps) for n in lens) + 3, rng)
+    pages = sum(-(-n // ps) for n in lens) + 3
+    table[3, 2], table[11 if ragged else 40, 0] = -1, pages
+    c = random_cache(fmt, pages, heads, ps, dim, None, junk=0x5A)
+    want = [t.cpu() if t is not None else None for t in (c.k, c.v, c.k_scales, c.v_scales)]
+    wide = vectors(rng, tokens, 2 * heads, dim, dtype=torch.float32).to(dtype)
+    dw = wide.to(DEV)
+    say("append many", fmt, dtype, ragged)
+    qbn.kv_append(c, dw[:, :heads], dw[:, heads:], table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                  None if cu is None else torch.from_numpy(cu).to(DEV))
+    torch.cuda.synchronize()
+    for which, x in ((0, wide[:, :heads]), (1, wide[:, heads:])):
+        code, scale = (None, None) if fmt == "bf16" else R.quantize(fmt, x.double().numpy())
+        if fmt == "mxfp4":
+            code = code[..., 0::2] | (code[..., 1::2] << 4)
+        t = 0
+        for b, n in enumerate(news):
+            for pos in range(lens[b] - n, lens[b]):
+                page = int(table[b, pos // ps]) if 0 <= pos < ps * row else -1
+                if 0 <= page < pages:
+                    want[which][0, page, :, pos % ps] = x[t].to(torch.bfloat16) if code is None else torch.from_numpy(code[t])
+                    if code is not None:
+                        want[which + 2][0, page, :, :, pos % ps] = torch.from_numpy(scale[t])
+                t += 1
+    for got, w, name in zip((c.k, c.v, c.k_scales, c.v_scales), want, ("k", "v", "k_scales", "v_scales")):
+        if w is not None:
+            assert torch.equal(got.cpu().view(torch.uint8), w.view(torch.uint8)), name
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
 def test_pages_beyond_32_bit_offsets(fmt):
     """The same tokens in the first and in the last pages of a cache whose K has
