@@ -383,6 +383,17 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         const auto turn = [&](int buf, Scores &x, Scores &y, Entries &e, Entries &f) {
             const int t3 = token_after(t2);
             const bool edge = is_edge(t1);
+            // One wave on a SIMD: the half of its 512 registers that only matrix
+            // instructions and copies reach holds what only matrix instructions
+            // use. Left to itself the compiler puts the scores there and stores
+            // others to memory (4096 tokens, 32 / 8 heads, bf16: 256 wide 599 us,
+            // so 345; 192 wide 285, so 278).
+            if constexpr (D > 128) {
+#pragma unroll
+                for (int t = 0; t < D / 32; ++t) asm volatile("" : "+a"(acc[t]));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) asm volatile("" : "+a"(q[k]));
+            }
             const float base = ref == kNegInf ? 0.0f : ref;
             Weights w;
             bf16x8 part[AHEAD];
