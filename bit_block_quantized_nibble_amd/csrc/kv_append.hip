@@ -76,8 +76,9 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
             load8<T>(src + (int64_t)min(first + t, a.b.tokens - 1) * (is_v ? a.vt : a.kt), raw[t]);
         // the sequences: how many of cu[1..seqs] are <= token
         int b[TOK], left[TOK], page[TOK], slot[TOK];
+        bool has[TOK];  // a row before cu[0] has no sequence, nor one that cu does not reach
 #pragma unroll
-        for (int t = 0; t < TOK; ++t) b[t] = a.b.cu ? 0 : first + t, left[t] = 1;
+        for (int t = 0; t < TOK; ++t) b[t] = a.b.cu ? 0 : first + t, left[t] = 1, has[t] = true;
         if (a.b.cu) {
             for (int i = 0; i < a.b.seqs; i += 64) {
                 const int end = i + lane < a.b.seqs ? a.b.cu[i + lane + 1] : 0x7FFFFFFF;
@@ -87,11 +88,15 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
                 if (n < 64) break;
             }
 #pragma unroll
-            for (int t = 0; t < TOK; ++t) left[t] = start_of(a.b, min(b[t], a.b.seqs - 1) + 1) - (first + t);
+            for (int t = 0; t < TOK; ++t) {
+                const int seq = min(b[t], a.b.seqs - 1);
+                has[t] = start_of(a.b, seq) <= first + t;
+                left[t] = start_of(a.b, seq + 1) - (first + t);
+            }
         }
 #pragma unroll
         for (int t = 0; t < TOK; ++t) {
-            const bool known = first + t < a.b.tokens && b[t] < a.b.seqs;  // or cu does not reach this token
+            const bool known = has[t] && first + t < a.b.tokens && b[t] < a.b.seqs;
             const int seq = min(b[t], a.b.seqs - 1);
             const int64_t pos = (int64_t)length_of(a.b, seq) - left[t];
             const bool in = known && pos >= 0 && (pos >> a.page_shift) < a.b.row;

@@ -97,7 +97,8 @@ QBN_API int64_t qbn_kv_bytes(int32_t format, int64_t layers, int64_t pages, int3
  * the rule of qbn_quantize_mx (exponent floor(log2 max|x|) - emax per 32,
  * elements rounded to nearest even and saturated; finite values). A token
  * whose table entry is not a page of the cache, or whose position is negative
- * or beyond the row, is not written (attention over it gives NaN). */
+ * or beyond the row, is not written (attention over it gives NaN), nor is a row
+ * that no sequence has (before cu[0], or from cu[seqs] on). */
 QBN_API int32_t qbn_kv_append(const qbn_kv_cache *cache, int64_t layer, const qbn_kv_batch *batch, const void *k,
                               int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
                               int64_t v_head_stride, int32_t dtype, void *stream);
