@@ -27,7 +27,8 @@
 // many units of 128 tokens a piece has follows from the lengths: so many that
 // about `blocks` pieces come out of all pairs, whatever the lengths. The
 // pieces of a pair are alike; each workgroup finds its own by a scan of the
-// lengths. A pair of one piece is written at once; the pieces of the others go
+// lengths, of many sequences by a search of the list that a first
+// kernel makes of them. A pair of one piece is written at once; the pieces of the others go
 // through the workspace, where the first of them notes which they are, and a
 // second kernel joins them in order. (Pieces that
 // run over the end of a pair into the next one would be more even, but the
@@ -62,6 +63,7 @@ struct DecodeArgs {
     float *lse;
     float *parts;  // pieces: [16][D] sums, then [16] maxima and [16] sums of weights
     int2 *found;   // per pair: its first piece, how many there are
+    int32_t *first;  // of more than kScanned sequences [seqs + 1]: pieces (of a pair) of those before
     float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
     uint32_t q_keep, q_flip;
     int group, tiles, rows;  // query heads per key-value head, 16-row tiles of them, pairs per sequence
@@ -86,52 +88,90 @@ __device__ __forceinline__ Span span_of(const DecodeArgs &a, int len) {
     return s;
 }
 
+// Pieces of a pair of n units; a sequence without tokens has outputs to be written, too.
+__device__ __forceinline__ uint32_t pieces_of(int n, uint32_t per) { return n == 0 ? 1 : ((uint32_t)n + per - 1) / per; }
+
+// Units of a piece at most, from the units of all sequences: about `blocks`
+// pieces of all pairs. Rounded up pair by pair, that may be a few pieces more
+// than run at once, and those would double the time: longer pieces, until
+// all fit. count(per): the pieces of all sequences (fewer than 2^31 / rows).
+template <typename Count>
+__device__ __forceinline__ uint32_t plan_pieces(const DecodeArgs &a, int64_t total, Count count) {
+    const int64_t most = div_i64(total * a.rows + a.blocks - 1, a.blocks);
+    uint32_t per = (uint32_t)(most < 1 ? 1 : most < (1 << 24) ? most : 1 << 24);
+    for (int i = 0; i < 8 && (int64_t)a.b.seqs * a.rows <= a.blocks; ++i) {
+        const int64_t pieces = count(per) * a.rows;
+        if (pieces <= a.blocks) break;
+        per = max(per + 1, (uint32_t)div_i64(per * pieces + a.blocks - 1, a.blocks));
+    }
+    return per;
+}
+
 // Units and pieces of the sequences, 64 at a time: each wave scans the lengths
 // for itself, which costs a load and a few lane moves and no barrier.
 struct Chunk {
-    int n, upto, all;  // of this lane's sequence, up to and with it, of all 64
+    int len, n, upto, all;  // of this lane's sequence: its length, its pieces; pieces up to and with it, of all 64
 };
-__device__ __forceinline__ Chunk scan_of(int n) {
-    Chunk c;
-    c.n = n;
-    c.upto = wave_scan(n);
-    c.all = __builtin_amdgcn_readlane(c.upto, 63);
-    return c;
-}
 __device__ __forceinline__ int length_at(const DecodeArgs &a, int s0) {  // of this lane's sequence
     const int s = s0 + (threadIdx.x & 63);
     return s < a.b.seqs ? a.b.lens[s] : 0;
 }
-__device__ __forceinline__ uint32_t pieces_at(const DecodeArgs &a, int s0, int len, uint32_t per) {  // of this lane's sequence
-    if (s0 + (int)(threadIdx.x & 63) >= a.b.seqs) return 0;
-    const uint32_t n = (uint32_t)span_of(a, len).n;
-    return n == 0 ? 1 : (n + per - 1) / per;  // a sequence without tokens has outputs to be written, too
+__device__ __forceinline__ Chunk pieces_at(const DecodeArgs &a, int s0, int len, uint32_t per) {
+    Chunk c;
+    c.len = len;
+    c.n = s0 + (int)(threadIdx.x & 63) < a.b.seqs ? (int)pieces_of(span_of(a, len).n, per) : 0;
+    c.upto = wave_scan(c.n);
+    c.all = __builtin_amdgcn_readlane(c.upto, 63);
+    return c;
 }
 
 struct Plan {
-    int first;     // lengths of sequences 0 .. 63, one per lane
-    Chunk pieces;  // of those
+    Chunk first;   // of sequences 0 .. 63
     uint32_t per;  // units of a piece at most
 };
 __device__ __forceinline__ Plan plan_units(const DecodeArgs &a) {
     Plan p;
-    p.first = length_at(a, 0);
-    int64_t total = scan_of(span_of(a, p.first).n).all;  // a sequence has less than 2^24 units
-    for (int s = 64; s < a.b.seqs; s += 64) total += scan_of(span_of(a, length_at(a, s)).n).all;
-    const int64_t per = div_i64(total * a.rows + a.blocks - 1, a.blocks);
-    p.per = (uint32_t)(per < 1 ? 1 : per < (1 << 24) ? per : 1 << 24);
-    // Rounded up pair by pair, that may be a few pieces more than run at once,
-    // and those would double the time: longer pieces, until all fit.
-    p.pieces = scan_of(pieces_at(a, 0, p.first, p.per));
-    for (int i = 0; i < 8 && (int64_t)a.b.seqs * a.rows <= a.blocks; ++i) {
-        int64_t pieces = p.pieces.all;
-        for (int s = 64; s < a.b.seqs; s += 64) pieces += scan_of(pieces_at(a, s, length_at(a, s), p.per)).all;
-        pieces *= a.rows;  // fewer than 2^31
-        if (pieces <= a.blocks) break;
-        p.per = max(p.per + 1, (uint32_t)div_i64(p.per * pieces + a.blocks - 1, a.blocks));
-        p.pieces = scan_of(pieces_at(a, 0, p.first, p.per));
-    }
+    const int len = length_at(a, 0);
+    const auto units = [&](int len) { return __builtin_amdgcn_readlane(wave_scan(span_of(a, len).n), 63); };  // each less than 2^24
+    int64_t total = units(len);
+    for (int s = 64; s < a.b.seqs; s += 64) total += units(length_at(a, s));
+    const auto count = [&](uint32_t per) {
+        p.first = pieces_at(a, 0, len, per);
+        int64_t n = p.first.all;
+        for (int s = 64; s < a.b.seqs; s += 64) n += pieces_at(a, s, length_at(a, s), per).all;
+        return n;
+    };
+    p.per = plan_pieces(a, total, count);
+    p.first = pieces_at(a, 0, len, p.per);
     return p;
+}
+
+// Many sequences: one workgroup lists the pieces before each sequence, and the
+// others search the list.
+constexpr int kPlanThreads = 1024;
+__global__ __launch_bounds__(kPlanThreads) void k_decode_plan(DecodeArgs a) {
+    __shared__ int64_t s_scan[kPlanThreads / 64 + 1];
+    const auto sum = [&](int64_t mine) {
+        int64_t total;
+        block_scan<kPlanThreads>(mine, s_scan, total);
+        return total;
+    };
+    int64_t mine = 0;
+    for (int s = threadIdx.x; s < a.b.seqs; s += kPlanThreads) mine += span_of(a, a.b.lens[s]).n;
+    const uint32_t per = plan_pieces(a, sum(mine), [&](uint32_t per) {
+        int64_t n = 0;
+        for (int s = threadIdx.x; s < a.b.seqs; s += kPlanThreads) n += pieces_of(span_of(a, a.b.lens[s]).n, per);
+        return sum(n);
+    });
+    int64_t before = 0;
+    for (int s0 = 0; s0 < a.b.seqs; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        int64_t all;
+        const int64_t at = block_scan<kPlanThreads>(s < a.b.seqs ? pieces_of(span_of(a, a.b.lens[s]).n, per) : 0, s_scan, all);
+        if (s < a.b.seqs) a.first[s] = (int)(before + at);  // fewer than the main kernel's workgroups
+        before += all;
+    }
+    if (threadIdx.x == 0) a.first[a.b.seqs] = (int)before;
 }
 
 // A wave's 32 tokens as loaded. A vector memory instruction takes a compute
@@ -411,23 +451,31 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
         r = blockIdx.x % a.rows;
         len = length_of(a.b, b);
     } else {
-        const Plan p = plan_units(a);
-        int lens = p.first;
-        Chunk c = p.pieces;
-        int64_t before = 0;
-        int s0 = 0;
-        while (blockIdx.x >= (before + c.all) * a.rows) {
-            before += c.all;
-            s0 += 64;
-            if (s0 >= a.b.seqs) return;  // more workgroups than pieces
-            lens = length_at(a, s0);
-            c = scan_of(pieces_at(a, s0, lens, p.per));
+        int before;  // pieces of a pair of the sequences before
+        if (a.first != nullptr) {
+            b = count_upto(a.first, a.b.seqs, blockIdx.x / a.rows);
+            if (b >= a.b.seqs) return;  // more workgroups than pieces
+            before = a.first[b];
+            pieces = a.first[b + 1] - before;
+            len = length_of(a.b, b);
+        } else {
+            const Plan p = plan_units(a);
+            Chunk c = p.first;
+            int s0 = 0;
+            before = 0;
+            while (blockIdx.x >= (uint32_t)(before + c.all) * a.rows) {
+                before += c.all;
+                s0 += 64;
+                if (s0 >= a.b.seqs) return;
+                c = pieces_at(a, s0, length_at(a, s0), p.per);
+            }
+            const int at = __builtin_ctzll(__ballot(blockIdx.x < (uint32_t)(before + c.upto) * a.rows));
+            b = s0 + at;
+            len = __builtin_amdgcn_readlane(c.len, at);
+            pieces = __builtin_amdgcn_readlane(c.n, at);
+            before += __builtin_amdgcn_readlane(c.upto, at) - pieces;
         }
-        const int at = __builtin_ctzll(__ballot(blockIdx.x < (before + c.upto) * a.rows));
-        b = s0 + at;
-        len = __builtin_amdgcn_readlane(lens, at);
-        pieces = __builtin_amdgcn_readlane(c.n, at);
-        const uint32_t rest = (uint32_t)(blockIdx.x - (before + __builtin_amdgcn_readlane(c.upto, at) - pieces) * a.rows);
+        const uint32_t rest = blockIdx.x - (uint32_t)before * a.rows;
         r = rest / pieces;
         piece = rest % pieces;
         if (piece == 0 && tid == 0) a.found[(int64_t)b * a.rows + r] = int2{(int)blockIdx.x, pieces};
@@ -646,9 +694,14 @@ int64_t most_pieces(const Cut &p) {
     return p.pairs * p.units < most ? p.pairs * p.units : most;
 }
 
+// Bytes of the pieces and of the list of where they are, and with the list of
+// the sequences' first ones.
+int64_t piece_bytes(const Cut &p, int head_dim) { return most_pieces(p) * (16 * (int64_t)head_dim + 32) * 4 + p.pairs * 8; }
+
 template <int F>
 hipError_t launch(const DecodeArgs &a, int64_t grid, hipStream_t s) {
     const dim3 g((unsigned)grid);
+    if (a.first) k_decode_plan<<<1, kPlanThreads, 0, s>>>(a);
     const int64_t rows = (int64_t)a.b.seqs * a.rows / a.tiles * a.group;
 #define QBN_KV_DIM(DD)                                            \
     case DD:                                                      \
@@ -672,7 +725,8 @@ hipError_t launch(const DecodeArgs &a, int64_t grid, hipStream_t s) {
 
 int64_t kv_decode_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     const Cut p = plan_of(c, b, q_heads, window, sinks);
-    return p.blocks ? most_pieces(p) * (16 * (int64_t)c.head_dim + 32) * 4 + p.pairs * 8 : 0;
+    if (p.blocks == 0) return 0;
+    return piece_bytes(p, c.head_dim) + (b.seqs > kScanned ? 4 * (b.seqs + 1) : 0);
 }
 
 hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, int q_heads, const KvRows &q,
@@ -690,6 +744,7 @@ hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_b
     a.out = (__bf16 *)out, a.lse = lse;
     a.parts = p.blocks ? (float *)ws : nullptr;
     a.found = p.blocks ? (int2 *)(a.parts + most_pieces(p) * (16 * c.head_dim + 32)) : nullptr;
+    a.first = p.blocks && b.seqs > kScanned ? (int32_t *)((uint8_t *)ws + piece_bytes(p, c.head_dim)) : nullptr;
     a.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
     a.q_keep = scale == 0.0f ? 0u : ~0u;
     a.q_flip = scale < 0.0f ? 0x80008000u : 0u;

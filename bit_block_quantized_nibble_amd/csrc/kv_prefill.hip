@@ -45,6 +45,7 @@ struct PrefillArgs {
     int64_t qt, qh;
     __bf16 *out;
     float *lse;
+    int32_t *first;  // of more than kScanned sequences with cu [seqs + 1]: row tiles of those before
     float *parts;  // [splits][tokens][heads][D] sums, then [splits][tokens][heads] references and weight sums
     float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
     uint32_t q_keep, q_flip;
@@ -82,6 +83,27 @@ __device__ __forceinline__ int new_tokens(const Batch &b, int s, int &first) {
     return x >= 0 && y >= x && y <= b.tokens ? y - x : 0;
 }
 
+__device__ __forceinline__ int64_t row_tiles(int fresh, int group, int bm) {  // < 2^24
+    return ((int64_t)fresh * group + bm - 1) / bm;
+}
+
+// Many sequences: one workgroup lists the row tiles before each, and
+// the others search the list.
+constexpr int kPlanThreads = 1024;
+__global__ __launch_bounds__(kPlanThreads) void k_prefill_plan(PrefillArgs a, int bm) {
+    __shared__ int64_t s_scan[kPlanThreads / 64 + 1];
+    int64_t before = 0;
+    for (int s0 = 0; s0 < a.b.seqs; s0 += kPlanThreads) {
+        const int s = s0 + threadIdx.x;
+        int x;
+        int64_t all;
+        const int64_t at = block_scan<kPlanThreads>(s < a.b.seqs ? row_tiles(new_tokens(a.b, s, x), a.group, bm) : 0, s_scan, all);
+        if (s < a.b.seqs) a.first[s] = (int)min(before + at, (int64_t)0x7FFFFFFF);  // beyond the grid: cu is out of order
+        before += all;
+    }
+    if (threadIdx.x == 0) a.first[a.b.seqs] = (int)min(before, (int64_t)0x7FFFFFFF);
+}
+
 // One element of V, as the tiles see it.
 template <int F, int D>
 __device__ __forceinline__ float element(const Cache &c, int64_t head, int ps, int slot, int d) {
@@ -105,31 +127,43 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     const int kv_head = blockIdx.x % a.c.heads;
     const int want = blockIdx.x / a.c.heads;  // row tile in the list of all sequences'
 
-    // ---- which sequence and row tile: each wave scans the sequences for itself, 64 at a time
+    // ---- which sequence and row tile (of a sequence's, the longest rows first)
     int b, tile, q0, fresh, len;
-    for (int64_t before = 0, s0 = 0;; s0 += 64) {
-        if (s0 >= a.b.seqs) return;
-        const int s = (int)s0 + lane;
-        int x = 0, n = 0, l = 0;
-        if (s < a.b.seqs) {
-            n = new_tokens(a.b, s, x);
-            l = a.b.lens[s];
+    if (!a.b.cu) {  // one token each: as many tiles each
+        const int each = (a.group + L::BM - 1) / L::BM;
+        b = want / each, tile = each - 1 - want % each;
+        if (b >= a.b.seqs) return;
+        q0 = b, fresh = 1, len = length_of(a.b, b);
+    } else if (a.first != nullptr) {
+        b = count_upto(a.first, a.b.seqs, want);
+        if (b >= a.b.seqs) return;
+        fresh = new_tokens(a.b, b, q0);
+        tile = (int)row_tiles(fresh, a.group, L::BM) - 1 - (want - a.first[b]);
+        len = length_of(a.b, b);
+    } else {  // each wave scans the sequences for itself, 64 at a time
+        for (int before = 0, s0 = 0;; s0 += 64) {
+            if (s0 >= a.b.seqs) return;
+            const int s = s0 + lane;
+            int x = 0, n = 0, l = 0;
+            if (s < a.b.seqs) n = new_tokens(a.b, s, x), l = a.b.lens[s];
+            const int upto = wave_scan((int)row_tiles(n, a.group, L::BM));
+            const uint64_t here = __ballot(want < before + upto);
+            if (here == 0) {
+                before += __builtin_amdgcn_readlane(upto, 63);
+                continue;
+            }
+            const int at = __builtin_ctzll(here);
+            b = s0 + at;
+            tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - want;
+            q0 = __builtin_amdgcn_readlane(x, at);
+            fresh = __builtin_amdgcn_readlane(n, at);
+            len = __builtin_amdgcn_readlane(l, at);
+            break;
         }
-        const int tiles = (int)(((int64_t)n * a.group + L::BM - 1) / L::BM);  // < 2^24
-        const int upto = wave_scan(tiles);
-        const uint64_t here = __ballot(want < before + upto);
-        if (here == 0) {
-            before += __builtin_amdgcn_readlane(upto, 63);
-            continue;
-        }
-        const int at = __builtin_ctzll(here);
-        b = (int)s0 + at;
-        tile = (int)(before + __builtin_amdgcn_readlane(upto, at) - 1 - want);  // the longest rows first
-        q0 = __builtin_amdgcn_readlane(x, at);
-        fresh = __builtin_amdgcn_readlane(n, at);
-        len = __builtin_amdgcn_readlane(l, at);
-        break;
     }
+    b = __builtin_amdgcn_readfirstlane(b), tile = __builtin_amdgcn_readfirstlane(tile);
+    q0 = __builtin_amdgcn_readfirstlane(q0), fresh = __builtin_amdgcn_readfirstlane(fresh);
+    len = __builtin_amdgcn_readfirstlane(len);
     const int rows = fresh * a.group;
     const int r0 = tile * L::BM;
     const int ps = 1 << a.c.page_shift;
@@ -559,7 +593,9 @@ struct Plan {
 Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     Plan p;
     const int64_t group = q_heads / c.heads;
-    p.waves = c.head_dim <= 128 && b.tokens * group / 256 * c.heads >= 256 ? 8 : 4;
+    // Tiles of 256 rows where they fill the compute units and the sequences fill
+    // them (65536 sequences of one row, 4 heads of 64: 6.6 ms, in tiles of 128 rows 3.1).
+    p.waves = c.head_dim <= 128 && b.tokens * group / 256 * c.heads >= 256 && b.tokens * group >= 256 * b.seqs ? 8 : 4;
     const int BM = p.waves * 32;
     p.tiles = b.cu ? b.tokens * group / BM + b.seqs : b.seqs * ((group + BM - 1) / BM);
     int64_t units = (b.row * c.page_size + BN - 1) / BN;
@@ -578,6 +614,11 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
     return p;
 }
 
+int64_t part_bytes(const Plan &p, const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads) {
+    return p.splits > 1 ? p.splits * b.tokens * q_heads * ((int64_t)c.head_dim + 2) * 4 : 0;
+}
+bool listed(const qbn_kv_batch &b) { return b.cu && b.seqs > kScanned; }
+
 template <int F>
 hipError_t launch(const PrefillArgs &a, dim3 grid, int waves, hipStream_t s) {
     const int64_t total = (int64_t)a.b.tokens * a.c.heads * a.group;
@@ -590,6 +631,7 @@ hipError_t launch(const PrefillArgs &a, dim3 grid, int waves, hipStream_t s) {
             k_prefill_join<DD><<<(unsigned)((total + per - 1) / per), 256, 0, s>>>(a, total); \
         }                                                                      \
         break;
+    if (a.first) k_prefill_plan<<<1, kPlanThreads, 0, s>>>(a, waves * 32);
     switch (a.dim) {
         QBN_KV_DIM(64)
         QBN_KV_DIM(96)
@@ -605,7 +647,7 @@ hipError_t launch(const PrefillArgs &a, dim3 grid, int waves, hipStream_t s) {
 
 int64_t kv_prefill_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     const Plan p = plan_of(c, b, q_heads, window, sinks);
-    return p.splits > 1 ? p.splits * b.tokens * q_heads * ((int64_t)c.head_dim + 2) * 4 : 0;
+    return part_bytes(p, c, b, q_heads) + (listed(b) ? 4 * (b.seqs + 1) : 0);
 }
 
 hipError_t launch_kv_prefill(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, int q_heads, const KvRows &q,
@@ -622,6 +664,7 @@ hipError_t launch_kv_prefill(const qbn_kv_cache &c, int64_t layer, const qbn_kv_
     a.qt = q.token_stride, a.qh = q.head_stride;
     a.out = (__bf16 *)out, a.lse = lse;
     a.parts = (float *)ws;
+    a.first = listed(b) ? (int32_t *)((uint8_t *)ws + part_bytes(p, c, b, q_heads)) : nullptr;
     a.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
     a.q_keep = scale == 0.0f ? 0u : ~0u;
     a.q_flip = scale < 0.0f ? 0x80008000u : 0u;

@@ -8,7 +8,7 @@ import torch
 import bit_block_quantized_nibble_amd as qbn
 import kv_ref as R
 from gpu_util import DEV, say
-from test_gpu_kv_attention import FORMATS, random_cache, vectors
+from test_gpu_kv_attention import FORMATS, check, decode, fill, prefill, random_cache, vectors
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,88 @@ def test_append_leaves_rows_of_no_sequence_out(fmt, seqs, each):
     for got, w, name in zip((c.k, c.v, c.k_scales, c.v_scales), want, ("k", "v", "k_scales", "v_scales")):
         if w is not None:
             assert torch.equal(got.cpu().view(torch.uint8), w.view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("seqs,heads,group,dim", [(1, 1, 1, 64), (5, 2, 4, 128), (67, 1, 3, 96), (3, 1, 300, 64), (130, 2, 2, 256)])
+@pytest.mark.parametrize("window,sinks,wide", [(0, 0, False), (0, 0, True), (50, 3, True)])
+def test_prefill_of_one_token_each(fmt, seqs, heads, group, dim, window, sinks, wide):
+    """Without cu every sequence has one new token, as in decode."""
+    rng = np.random.default_rng(seqs + dim)
+    ps = 32
+    lens = [int(n) for n in rng.integers(0, 200, seqs)]
+    lens[0], lens[-1] = 1, 190
+    pages = sum(-(-n // ps) for n in lens) + 1
+    table = R.torch_table(lens, ps, 200 // ps + 1, pages, rng)
+    c = random_cache(fmt, pages, heads, ps, dim, rng)
+    fill(c, table, lens, rng)
+    if wide:
+        table = torch.cat([table, torch.full((seqs, 300), -1, dtype=torch.int32)], 1)
+    q = vectors(rng, seqs, heads * group, dim, gain=2.0)
+    say("prefill, one each", fmt, dim, seqs, window)
+    out, lse = qbn.kv_attention_prefill(c, q.to(DEV), None, table.to(DEV), ints(lens), window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    check(c, out, lse, q, table, lens, [1] * seqs, window, sinks)
+    # the same rows with cu written out
+    out, lse = prefill(c, q, list(range(seqs + 1)), table, lens, window=window, sinks=sinks)
+    check(c, out, lse, q, table, lens, [1] * seqs, window, sinks)
+
+
+@pytest.mark.parametrize("seqs", [1000, 4097])
+def test_thousands_of_sequences(seqs):
+    """Lengths and row lists of many sequences: empty ones, long ones at the ends
+    of a search's steps, decode and chunks, the same bits twice."""
+    rng = np.random.default_rng(seqs)
+    ps, dim, heads, group = 16, 64, 1, 2
+    lens = [int(x) for x in rng.integers(0, 30, seqs)]
+    for i, n in ((0, 0), (1, 900), (63, 500), (64, 0), (65, 1300), (seqs // 2, 2000), (seqs - 1, 1)):
+        lens[i] = n
+    news = [int(rng.integers(0, min(n, 3) + 1)) for n in lens]
+    pages = sum(-(-n // ps) for n in lens) + 1
+    table = R.torch_table(lens, ps, 2000 // ps + 1, pages, rng)
+    c = random_cache("mxfp8", pages, heads, ps, dim, rng)
+    fill(c, table, lens, rng)
+    q = vectors(rng, seqs, heads * group, dim, gain=2.0)
+    out, lse = decode(c, q, table, lens)
+    check(c, out, lse, q, table, lens, [1] * seqs, 0, 0)
+    again, lse2 = decode(c, q, table, lens)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    cu = [0] + np.cumsum(news).tolist()
+    q = vectors(rng, cu[-1], heads * group, dim, gain=2.0)
+    out, lse = prefill(c, q, cu, table, lens)
+    check(c, out, lse, q, table, lens, news, 0, 0)
+
+
+def test_calls_grow_with_the_sequences_not_with_their_square():
+    """Eight times as many sequences of one short context: the time may grow by
+    that factor and half of it again, not by its square."""
+    def times(seqs):
+        ps, dim, heads = 16, 64, 4
+        c = qbn.KVCache.empty("mxfp8", 1, seqs, heads, ps, dim, device=DEV)
+        for t in (c.k, c.v, c.k_scales, c.v_scales):
+            t.fill_(100)
+        table = torch.full((seqs, 64), -1, dtype=torch.int32, device=DEV)
+        table[:, 0] = torch.arange(seqs, device=DEV)
+        lens = torch.full((seqs,), 16, dtype=torch.int32, device=DEV)
+        x = torch.ones(seqs, heads, dim, dtype=torch.bfloat16, device=DEV)
+        cu = torch.arange(seqs + 1, dtype=torch.int32, device=DEV)
+        calls = [lambda: qbn.kv_append(c, x, x, table, lens, cu), lambda: qbn.kv_attention_decode(c, x, table, lens),
+                 lambda: qbn.kv_attention_prefill(c, x, cu, table, lens)]
+        got = []
+        for i, f in enumerate(calls):
+            say("many", seqs, ("append", "decode", "prefill")[i])
+            best = float("inf")
+            for _ in range(5):
+                a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+                a.record()
+                f()
+                b.record()
+                b.synchronize()
+                best = min(best, a.elapsed_time(b))
+            say("%.3f ms" % best)
+            got.append(best)
+        return got
+
+    few, many = times(8192), times(65536)
+    for name, a, b in zip(("append", "decode", "prefill"), few, many):
+        assert b <= 12 * a, "%s: %.3f ms for 8192 sequences, %.3f for 65536" % (name, a, b)
