@@ -45,7 +45,7 @@ struct PrefillArgs {
     int64_t qt, qh;
     __bf16 *out;
     float *lse;
-    int32_t *first;  // of more than kScanned sequences with cu [seqs + 1]: row tiles of those before
+    int32_t *first;  // of more than kScanned sequences with cu [seqs + 1]: row tiles of those before; then, whether cu is out of order
     float *parts;  // [splits][tokens][heads][D] sums, then [splits][tokens][heads] references and weight sums
     float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
     uint32_t q_keep, q_flip;
@@ -72,7 +72,7 @@ __device__ __forceinline__ T here(T v) {
     return v;
 }
 
-// A sequence's new tokens, as far as cu is in order and inside q.
+// A sequence's new tokens; -1 where cu is out of order or leaves q.
 __device__ __forceinline__ int new_tokens(const Batch &b, int s, int &first) {
     if (!b.cu) {
         first = s;
@@ -80,11 +80,11 @@ __device__ __forceinline__ int new_tokens(const Batch &b, int s, int &first) {
     }
     const int x = b.cu[s], y = b.cu[s + 1];
     first = x;
-    return x >= 0 && y >= x && y <= b.tokens ? y - x : 0;
+    return x >= 0 && y >= x && y <= b.tokens ? y - x : -1;
 }
 
 __device__ __forceinline__ int64_t row_tiles(int fresh, int group, int bm) {  // < 2^24
-    return ((int64_t)fresh * group + bm - 1) / bm;
+    return fresh < 0 ? 0 : ((int64_t)fresh * group + bm - 1) / bm;
 }
 
 // Many sequences: one workgroup lists the row tiles before each, and
@@ -93,15 +93,48 @@ constexpr int kPlanThreads = 1024;
 __global__ __launch_bounds__(kPlanThreads) void k_prefill_plan(PrefillArgs a, int bm) {
     __shared__ int64_t s_scan[kPlanThreads / 64 + 1];
     int64_t before = 0;
+    bool wrong = false;
     for (int s0 = 0; s0 < a.b.seqs; s0 += kPlanThreads) {
         const int s = s0 + threadIdx.x;
         int x;
         int64_t all;
-        const int64_t at = block_scan<kPlanThreads>(s < a.b.seqs ? row_tiles(new_tokens(a.b, s, x), a.group, bm) : 0, s_scan, all);
+        const int n = s < a.b.seqs ? new_tokens(a.b, s, x) : 0;
+        wrong |= n < 0;
+        const int64_t at = block_scan<kPlanThreads>(row_tiles(n, a.group, bm), s_scan, all);
         if (s < a.b.seqs) a.first[s] = (int)min(before + at, (int64_t)0x7FFFFFFF);  // beyond the grid: cu is out of order
         before += all;
     }
-    if (threadIdx.x == 0) a.first[a.b.seqs] = (int)min(before, (int64_t)0x7FFFFFFF);
+    wrong = __syncthreads_or(wrong);
+    if (threadIdx.x == 0) {
+        a.first[a.b.seqs] = (int)min(before, (int64_t)0x7FFFFFFF);
+        a.first[a.b.seqs + 1] = wrong;
+    }
+}
+
+// The outputs of the rows of q that no sequence has, before cu[0] and from
+// cu[seqs] on: 0 and -inf; of all rows NaN where cu is out of order. All
+// workgroups of the grid share them.
+template <int D>
+__device__ __forceinline__ void write_rest(const PrefillArgs &a, int lo, int hi, bool wrong) {
+    const int q_heads = a.c.heads * a.group;
+    const int64_t total = (int64_t)a.b.tokens * q_heads, shift = total * blockIdx.y;
+    const int64_t n = (int64_t)(wrong ? a.b.tokens : lo + (a.b.tokens - hi)) * q_heads;
+    const float sum = wrong ? __builtin_nanf("") : 0.0f;
+    float *st = a.parts + total * a.splits * D;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n * (D / 4); i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t k = i / (D / 4), row = wrong || k < (int64_t)lo * q_heads ? k : k + (int64_t)(hi - lo) * q_heads;
+        const int d = (int)(i % (D / 4)) * 4;
+        if (a.splits == 1) {
+            *reinterpret_cast<u32x2 *>(a.out + row * D + d) = u32x2{pack2(sum, sum), pack2(sum, sum)};
+            if (d == 0 && a.lse) a.lse[row] = wrong ? sum : kNegInf;
+        } else {
+            *reinterpret_cast<f32x4 *>(a.parts + (shift + row) * D + d) = f32x4{0, 0, 0, 0};
+            if (d == 0) {
+                st[shift + row] = kNegInf;
+                st[total * a.splits + shift + row] = sum;
+            }
+        }
+    }
 }
 
 // One element of V, as the tiles see it.
@@ -128,38 +161,44 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     const int want = blockIdx.x / a.c.heads;  // row tile in the list of all sequences'
 
     // ---- which sequence and row tile (of a sequence's, the longest rows first)
-    int b, tile, q0, fresh, len;
+    int b = a.b.seqs, tile = 0, q0 = 0, fresh = 0, len = 0;
     if (!a.b.cu) {  // one token each: as many tiles each
         const int each = (a.group + L::BM - 1) / L::BM;
         b = want / each, tile = each - 1 - want % each;
         if (b >= a.b.seqs) return;
         q0 = b, fresh = 1, len = length_of(a.b, b);
-    } else if (a.first != nullptr) {
-        b = count_upto(a.first, a.b.seqs, want);
-        if (b >= a.b.seqs) return;
-        fresh = new_tokens(a.b, b, q0);
-        tile = (int)row_tiles(fresh, a.group, L::BM) - 1 - (want - a.first[b]);
-        len = length_of(a.b, b);
-    } else {  // each wave scans the sequences for itself, 64 at a time
-        for (int before = 0, s0 = 0;; s0 += 64) {
-            if (s0 >= a.b.seqs) return;
-            const int s = s0 + lane;
-            int x = 0, n = 0, l = 0;
-            if (s < a.b.seqs) n = new_tokens(a.b, s, x), l = a.b.lens[s];
-            const int upto = wave_scan((int)row_tiles(n, a.group, L::BM));
-            const uint64_t here = __ballot(want < before + upto);
-            if (here == 0) {
-                before += __builtin_amdgcn_readlane(upto, 63);
-                continue;
+    } else {
+        const int lo = start_of(a.b, 0), hi = start_of(a.b, a.b.seqs);
+        bool wrong = false;
+        if (a.first != nullptr) {
+            wrong = a.first[a.b.seqs + 1] != 0;
+            b = count_upto(a.first, a.b.seqs, want);
+            if (b < a.b.seqs) {
+                fresh = new_tokens(a.b, b, q0);
+                tile = (int)row_tiles(fresh, a.group, L::BM) - 1 - (want - a.first[b]);
+                len = length_of(a.b, b);
             }
-            const int at = __builtin_ctzll(here);
-            b = s0 + at;
-            tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - want;
-            q0 = __builtin_amdgcn_readlane(x, at);
-            fresh = __builtin_amdgcn_readlane(n, at);
-            len = __builtin_amdgcn_readlane(l, at);
-            break;
+        } else {  // each wave scans the sequences for itself, 64 at a time
+            for (int before = 0, s0 = 0; s0 < a.b.seqs; s0 += 64) {
+                const int s = s0 + lane;
+                int x = 0, n = 0, l = 0;
+                if (s < a.b.seqs) n = new_tokens(a.b, s, x), l = a.b.lens[s];
+                wrong |= __any(n < 0);
+                const int upto = wave_scan((int)row_tiles(n, a.group, L::BM));
+                const uint64_t here = __ballot(want >= before && want < before + upto);
+                if (here) {
+                    const int at = __builtin_ctzll(here);
+                    b = s0 + at;
+                    tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - want;
+                    q0 = __builtin_amdgcn_readlane(x, at);
+                    fresh = __builtin_amdgcn_readlane(n, at);
+                    len = __builtin_amdgcn_readlane(l, at);
+                }
+                before += __builtin_amdgcn_readlane(upto, 63);
+            }
         }
+        if (wrong || lo > 0 || hi < a.b.tokens) write_rest<D>(a, lo, hi, wrong);
+        if (wrong || b >= a.b.seqs) return;
     }
     b = __builtin_amdgcn_readfirstlane(b), tile = __builtin_amdgcn_readfirstlane(tile);
     q0 = __builtin_amdgcn_readfirstlane(q0), fresh = __builtin_amdgcn_readfirstlane(fresh);
@@ -647,7 +686,7 @@ hipError_t launch(const PrefillArgs &a, dim3 grid, int waves, hipStream_t s) {
 
 int64_t kv_prefill_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     const Plan p = plan_of(c, b, q_heads, window, sinks);
-    return part_bytes(p, c, b, q_heads) + (listed(b) ? 4 * (b.seqs + 1) : 0);
+    return part_bytes(p, c, b, q_heads) + (listed(b) ? 4 * (b.seqs + 2) : 0);
 }
 
 hipError_t launch_kv_prefill(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, int q_heads, const KvRows &q,

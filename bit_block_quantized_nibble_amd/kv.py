@@ -231,7 +231,8 @@ def kv_attention_prefill(cache: KVCache, q: torch.Tensor, cu: Optional[torch.Ten
                          workspace: Optional[torch.Tensor] = None):
     """Causal attention of chunks of new tokens (already appended): rows
     cu[b] .. cu[b + 1] - 1 of q are the last tokens of sequence b, whose length
-    with them is lens[b]. Otherwise as kv_attention_decode."""
+    with them is lens[b]; rows before cu[0] and from cu[seqs] on are padding
+    (out = 0, lse = -inf). Otherwise as kv_attention_decode."""
     return _attention(False, cache, q, cu, table, lens, window, sinks, scale, layer, out, lse, workspace)
 
 

@@ -29,10 +29,10 @@
  * The batch. Row b of `table` lists the pages of sequence b: token t sits in
  * page table[b][t / page_size] at t % page_size. lens[b] counts the tokens
  * of sequence b INCLUDING the new ones of this step: of its new tokens, the
- * last one is at position lens[b] - 1. cu (int32 [seqs + 1], ascending,
- * cu[0] = 0, cu[seqs] = tokens) says which rows of q / k / v are the new
- * tokens of sequence b: cu[b] .. cu[b + 1] - 1. cu = NULL stands for one new
- * token per sequence.
+ * last one is at position lens[b] - 1. cu (int32 [seqs + 1], ascending, in
+ * 0 .. tokens) says which rows of q / k / v are the new tokens of sequence b:
+ * cu[b] .. cu[b + 1] - 1. Rows before cu[0] and from cu[seqs] on belong to no
+ * sequence (padding). cu = NULL stands for one new token per sequence.
  */
 #ifndef QBN_KV_H
 #define QBN_KV_H
@@ -109,12 +109,13 @@ QBN_API int32_t qbn_kv_append(const qbn_kv_cache *cache, int64_t layer, const qb
  *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)   (natural log).
  * Token j is visible if j <= p, j < lens[b], and (window == 0, or
  * j > p - window, or j < sinks): the last `window` tokens up to p itself, and
- * the first `sinks` ones. A query that sees nothing (lens[b] == 0, or more new
- * tokens than lens[b]) gives out = 0, lse = -inf. What is stored in tokens
- * that a query does not see, infinities and NaN included, never reaches its
- * output. If a visible token's table entry is not a page of the cache, or
- * lens[b] is negative or beyond the row, the outputs concerned are NaN (the
- * queries of that sequence's tile).
+ * the first `sinks` ones. A query that sees nothing (lens[b] == 0, more new
+ * tokens than lens[b], or a row of no sequence) gives out = 0, lse = -inf.
+ * What is stored in tokens that a query does not see, infinities and NaN
+ * included, never reaches its output. If a visible token's table entry is not
+ * a page of the cache, or lens[b] is negative or beyond the row, the outputs
+ * concerned are NaN (the queries of that sequence's tile). If cu does not
+ * ascend or leaves 0 .. tokens, all outputs are NaN.
  * q: QBN_BF16 with strides as in qbn_kv_append; out: bfloat16
  * [tokens][q_heads][head_dim], lse: binary32 [tokens][q_heads] or NULL.
  * q_heads % heads == 0. Products are exact, sums, softmax statistics and

@@ -51,6 +51,63 @@ def test_append_leaves_rows_of_no_sequence_out(fmt, seqs, each):
             assert torch.equal(got.cpu().view(torch.uint8), w.view(torch.uint8)), name
 
 
+@pytest.mark.parametrize("fmt,dim", [("bf16", 64), ("mxfp8", 96), ("mxfp4", 256)])
+@pytest.mark.parametrize("seqs", [1, 3, 64, 65, 130])
+@pytest.mark.parametrize("before,after", [(0, 37), (3, 0), (70, 300), (0, 0)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_prefill_rows_of_no_sequence(fmt, dim, seqs, before, after, wide):
+    """Padding around the sequences' rows sees nothing: 0 and -inf, in the whole
+    and in the split form, whatever out, lse and the workspace held."""
+    rng = np.random.default_rng(seqs + before + after)
+    ps, heads, group = 16, 1, 3
+    lens = [int(n) for n in rng.integers(0, 90, seqs)]
+    lens[0] = 77
+    news = [int(rng.integers(0, min(n, 9) + 1)) for n in lens]
+    pages = sum(-(-n // ps) for n in lens) + 1
+    table = R.torch_table(lens, ps, 6, pages, rng)
+    c = random_cache(fmt, pages, heads, ps, dim, rng)
+    fill(c, table, lens, rng)
+    cu = before + np.concatenate([[0], np.cumsum(news)])
+    tokens = int(cu[-1]) + after
+    if tokens == 0:
+        return
+    q = vectors(rng, tokens, heads * group, dim, gain=2.0)
+    if wide:  # room for many pages: the split form
+        table = torch.cat([table, torch.full((seqs, 400), -1, dtype=torch.int32)], 1)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    ws = torch.full((16 << 20,), 7.0, device=DEV)
+    prefill(c, q, cu.tolist(), table, lens, out=out, lse=lse, workspace=ws)
+    a, b = int(cu[0]), int(cu[-1])
+    for rows in (slice(0, a), slice(b, tokens)):
+        assert (out[rows] == 0).all() and (lse[rows] == -float("inf")).all()
+    check(c, out[a:b], lse[a:b], q[a:b], table, lens, news, 0, 0)
+
+
+@pytest.mark.parametrize("cu", [
+    [0, 5, 3, 8], [0, 3, 5, 9], [-1, 3, 5, 8], [2, 1, 0, 8], [8, 8, 8, 0], [0, 2 ** 31 - 1, 4, 8], [0, -2 ** 31, 4, 8],
+    [5, 3, 2, 1],
+])
+@pytest.mark.parametrize("seqs", [3, 67])
+@pytest.mark.parametrize("wide", [False, True])
+def test_prefill_rows_out_of_order_give_nan(cu, seqs, wide):
+    """A cu that does not ascend, or leaves q: every output is NaN, none is left as it was."""
+    rng = np.random.default_rng(seqs)
+    ps, dim, tokens = 16, 64, 8
+    cu = cu + [cu[-1]] * (seqs - 3)
+    lens = [40] * seqs
+    table = R.torch_table(lens, ps, 3, 3 * seqs, rng)
+    c = random_cache("mxfp8", 3 * seqs, 1, ps, dim, rng)
+    fill(c, table, lens, rng)
+    if wide:
+        table = torch.cat([table, torch.full((seqs, 400), -1, dtype=torch.int32)], 1)
+    q = vectors(rng, tokens, 2, dim)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    prefill(c, q, cu, table, lens, out=out, lse=lse, workspace=torch.full((16 << 20,), 7.0, device=DEV))
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("seqs,heads,group,dim", [(1, 1, 1, 64), (5, 2, 4, 128), (67, 1, 3, 96), (3, 1, 300, 64), (130, 2, 2, 256)])
 @pytest.mark.parametrize("window,sinks,wide", [(0, 0, False), (0, 0, True), (50, 3, True)])
