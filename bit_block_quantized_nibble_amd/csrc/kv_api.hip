@@ -104,7 +104,8 @@ int32_t check_pools(const qbn_kv_pool *in, const qbn_kv_pool *out, int64_t count
 }
 
 int32_t check_workspace(const void *ws, int64_t have, int64_t need) {
-    if (need <= 0) return QBN_OK;
+    if (need < 0) return QBN_ERR_SHAPE;
+    if (need == 0) return QBN_OK;
     if (!ws) return QBN_ERR_NULL;
     if (!aligned(ws, 16)) return QBN_ERR_ALIGN;
     return have < need ? QBN_ERR_SHAPE : QBN_OK;

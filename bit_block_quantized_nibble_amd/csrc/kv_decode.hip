@@ -725,6 +725,8 @@ hipError_t launch(const DecodeArgs &a, int64_t grid, hipStream_t s) {
 
 int64_t kv_decode_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     const Cut p = plan_of(c, b, q_heads, window, sinks);
+    const int64_t rows = b.seqs * q_heads, joins = rows < 1024 ? rows : (rows + 3) / 4;
+    if ((p.blocks ? most_pieces(p) : p.pairs) >= kGridThreads / 256 || (p.blocks && joins >= kGridThreads / 256)) return -1;
     if (p.blocks == 0) return 0;
     return piece_bytes(p, c.head_dim) + (b.seqs > kScanned ? 4 * (b.seqs + 1) : 0);
 }

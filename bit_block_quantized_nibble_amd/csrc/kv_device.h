@@ -9,6 +9,8 @@ namespace kv {
 
 enum Fmt { BF16 = 0, FP8 = 1, FP4 = 2 };
 
+constexpr int64_t kGridThreads = (int64_t)1 << 32;  // a launch has fewer threads along x
+
 template <int F>
 constexpr int kBits = F == BF16 ? 16 : F == FP8 ? 8 : 4;
 

@@ -17,6 +17,7 @@ struct KvRows {  // [token][head] vectors of head_dim elements, strides in eleme
 hipError_t launch_kv_append(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, const KvRows &k,
                             const KvRows &v, int dtype, hipStream_t s);
 
+// Bytes of a call's workspace; -1 where a launch would pass the 2^32 threads of a grid.
 int64_t kv_decode_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks);
 hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_batch &b, int q_heads, const KvRows &q,
                             float scale, int window, int sinks, void *out, float *lse, void *ws, hipStream_t s);

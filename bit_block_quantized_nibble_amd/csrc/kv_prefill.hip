@@ -686,6 +686,7 @@ hipError_t launch(const PrefillArgs &a, dim3 grid, int waves, hipStream_t s) {
 
 int64_t kv_prefill_workspace(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     const Plan p = plan_of(c, b, q_heads, window, sinks);
+    if (p.tiles * c.heads >= kGridThreads / (p.waves * 64)) return -1;
     return part_bytes(p, c, b, q_heads) + (listed(b) ? 4 * (b.seqs + 2) : 0);
 }
 

@@ -125,7 +125,9 @@ QBN_API int32_t qbn_kv_append(const qbn_kv_cache *cache, int64_t layer, const qb
  * The work is split over a sequence's length where there are few sequences;
  * the pieces go through `workspace` (device, 16-byte aligned, at least
  * qbn_kv_attention_workspace bytes, not kept: it may be shared by calls that
- * follow each other on a stream). */
+ * follow each other on a stream). That function gives -1, and the calls
+ * QBN_ERR_SHAPE, also where a launch would have 2^32 threads or more (from
+ * about 2^24 pairs of a sequence and 16 query heads of a key-value head on). */
 QBN_API int64_t qbn_kv_attention_workspace(const qbn_kv_cache *cache, const qbn_kv_batch *batch, int32_t q_heads,
                                            int32_t window, int32_t sinks, int32_t decode);
 
