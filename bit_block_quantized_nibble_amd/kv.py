@@ -101,6 +101,16 @@ def _call():
     return _calls
 
 
+def _fixed(name: str, doc: str):
+    """An attribute that stays the same tensor: the handle of a cache or pool
+    holds its address. (`x.lens += 1` works in place and assigns the same one.)"""
+    def put(self, t):
+        if t is not getattr(self, "_" + name):
+            raise AttributeError("%s is fixed for the life of the handle: write into it, or make another" % name)
+
+    return property(lambda self: getattr(self, "_" + name), put, doc=doc)
+
+
 def _first_device(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("the tensors of a cache or pool must be device (cuda) tensors")
@@ -115,6 +125,11 @@ class KVCache:
     ("mxfp4"); k_scales, v_scales: uint8 E8M0 [layers][pages][heads]
     [head_dim / 32][page_size] for the last two. The tensors are kept and used
     in place; they are fixed for the life of the handle."""
+
+    k = _fixed("k", "Elements of K.")
+    v = _fixed("v", "Elements of V.")
+    k_scales = _fixed("k_scales", "E8M0 scales of K, or None.")
+    v_scales = _fixed("v_scales", "E8M0 scales of V, or None.")
 
     def __init__(self, format: str, k: torch.Tensor, v: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
                  v_scales: Optional[torch.Tensor] = None):
@@ -146,7 +161,7 @@ class KVCache:
         for t, name in parts:
             if t.get_device() != self.index:
                 raise ValueError("%s is on %s, the cache on another device" % (name, t.device))
-        self.format, self.k, self.v, self.k_scales, self.v_scales = format, k, v, k_scales, v_scales
+        self.format, self._k, self._v, self._k_scales, self._v_scales = format, k, v, k_scales, v_scales
         self.layers, self.pages, self.heads, self.page_size, self.head_dim = layers, pages, heads, page, dim
         self.device, self.scale = k.device, 1.0 / math.sqrt(dim)
         self._handle = bytes(_CCache(
@@ -172,11 +187,16 @@ class KVCache:
 class KVPool:
     """Which pages each sequence slot has: table int32 [seqs][row] (a page or
     -1), lens int32 [seqs] (tokens), refs int32 [pages] (how many entries name
-    the page; 0 is free)."""
+    the page; 0 is free). The tensors are kept and used in place; they are fixed
+    for the life of the handle (write into them, or make another pool)."""
+
+    table = _fixed("table", "Pages of each slot, or -1.")
+    lens = _fixed("lens", "Tokens of each slot.")
+    refs = _fixed("refs", "How many entries name each page.")
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int):
         self._handle, self.index = (_calls or _call()).pool(table, lens, refs, page_size)
-        self.table, self.lens, self.refs, self.page_size = table, lens, refs, page_size
+        self._table, self._lens, self._refs, self.page_size = table, lens, refs, page_size
 
     @classmethod
     def empty(cls, seqs: int, row: int, pages: int, page_size: int, device="cuda") -> "KVPool":
@@ -189,7 +209,8 @@ class KVPool:
     def like(cls, other: "KVPool") -> "KVPool":
         """Uninitialized tables of the same sizes, as `out` of the calls below."""
         p = cls.__new__(cls)
-        p.table, p.lens, p.refs, p._handle = (_calls or _call()).pool_like(other.table, other.lens, other.refs, other.page_size)
+        p._table, p._lens, p._refs, p._handle = (_calls or _call()).pool_like(other._table, other._lens, other._refs,
+                                                                              other.page_size)
         p.page_size, p.index = other.page_size, other.index
         return p
 
@@ -283,4 +304,4 @@ def kv_compact(cache: KVCache, pool: KVPool, out: Optional[KVPool] = None, live:
     """Pack the pool: the L pages in use end up in pages 0 .. L - 1 of every
     layer, the tables follow. Returns L as a device int32."""
     return _result((_calls or _call()).compact(cache._handle, pool._handle, _out(pool, out, cache)._handle, pool.index,
-                                               pool.table, live, workspace), "qbn_kv_compact")
+                                               pool._table, live, workspace), "qbn_kv_compact")
