@@ -440,9 +440,12 @@ Pool pool_of(const qbn_kv_pool &p) {
     return {(int)p.seqs, (int)p.row, (int)p.pages, __builtin_ctz(p.page_size), p.table, p.lens, p.refs};
 }
 
+// All three, since the pointer of a tensor without elements is null.
+bool same(const qbn_kv_pool &a, const qbn_kv_pool &b) { return a.table == b.table && a.lens == b.lens && a.refs == b.refs; }
+
 // out = in, where they are not the same tables.
 void copy_pool(const qbn_kv_pool &in, const qbn_kv_pool &out, hipStream_t s) {
-    if (in.table == out.table) return;
+    if (same(in, out)) return;
     const int64_t most = in.seqs * in.row > in.pages ? in.seqs * in.row : in.pages;
     const int64_t blocks = (most + 255) / 256;
     if (most > 0 || in.seqs > 0)
@@ -479,7 +482,7 @@ hipError_t launch_kv_fork(const qbn_kv_cache &c, const qbn_kv_pool &in, const qb
 
 hipError_t launch_kv_free(const qbn_kv_pool &in, const qbn_kv_pool &out, int64_t count, const int32_t *rows,
                           int window, int sinks, hipStream_t s) {
-    if (in.table != out.table && in.seqs * in.row <= kFreeTable && in.pages <= kFreePages && in.seqs <= kFreeSlots && count <= kFreeSlots) {
+    if (!same(in, out) && in.seqs * in.row <= kFreeTable && in.pages <= kFreePages && in.seqs <= kFreeSlots && count <= kFreeSlots) {
         k_copy_free<<<1, kThreads, 0, s>>>(pool_of(in), pool_of(out), (int)count, rows, window, sinks);
         return hipGetLastError();
     }
