@@ -7,6 +7,7 @@
 // see (devices, types, sizes) with the words of kv.py's other checks, allocates
 // what the caller did not give, and returns the C ABI's status.
 #include <Python.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
 
@@ -141,8 +142,8 @@ PyObject *guarded(F f) {
     try {
         return f();
     } catch (const Refused &) {
-    } catch (const std::exception &e) {  // torch's allocator
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // torch's, the allocator's torch.OutOfMemoryError above all: as torch's own functions raise it
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }
