@@ -83,18 +83,57 @@ qbn_kv_batch batch(int64_t dev, int64_t tokens, const at::Tensor &table, const a
     return b;
 }
 
-// torch's current stream of a device, as torch._C._cuda_getCurrentRawStream gives it.
-PyObject *g_raw_stream = nullptr;
-void *stream_of(int64_t dev) {
+// torch's current stream of a device, and the exchange of the current device for
+// another (-1: none) and back, as torch's Python gives them.
+PyObject *g_raw_stream = nullptr, *g_exchange = nullptr, *g_exchange_back = nullptr;
+
+PyObject *with_index(PyObject *f, int64_t dev) {
     PyObject *arg = PyLong_FromLongLong(dev);
-    PyObject *r = arg ? PyObject_CallOneArg(g_raw_stream, arg) : nullptr;
+    PyObject *r = arg ? PyObject_CallOneArg(f, arg) : nullptr;
     Py_XDECREF(arg);
-    if (!r) throw Refused{};
-    void *s = PyLong_AsVoidPtr(r);
-    Py_DECREF(r);
-    if (!s && PyErr_Occurred()) throw Refused{};
-    return s;
+    return r;
 }
+
+// A call's stream, with its device as the current one while this lives: the
+// default stream's handle is 0 on every device, and a launch on it goes to the
+// current one.
+class OnDevice {
+  public:
+    explicit OnDevice(int64_t dev) {
+        PyObject *r = with_index(g_exchange, dev);
+        if (!r) throw Refused{};
+        before_ = PyLong_AsLongLong(r);
+        Py_DECREF(r);
+        moved_ = before_ >= 0 && before_ != dev;
+        r = with_index(g_raw_stream, dev);
+        if (r) {
+            stream_ = PyLong_AsVoidPtr(r);
+            Py_DECREF(r);
+        }
+        if (!stream_ && PyErr_Occurred()) {
+            back();
+            throw Refused{};
+        }
+    }
+    OnDevice(const OnDevice &) = delete;
+    ~OnDevice() { back(); }
+    operator void *() const { return stream_; }
+
+  private:
+    void back() {
+        if (!moved_) return;
+        moved_ = false;
+        PyObject *type, *value, *trace;  // an error on its way is kept
+        PyErr_Fetch(&type, &value, &trace);
+        PyObject *r = with_index(g_exchange_back, before_);
+        if (r) Py_DECREF(r);
+        else PyErr_WriteUnraisable(g_exchange_back);
+        PyErr_Restore(type, value, trace);
+    }
+    int64_t before_ = -1;
+    bool moved_ = false;
+    void *stream_ = nullptr;
+};
 
 int64_t integer(PyObject *o) {
     const long long v = PyLong_AsLongLong(o);
@@ -167,7 +206,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {  // cache, devi
         if (v.t.scalar_type() != t || v.t.size(0) != k.t.size(0)) refuse(PyExc_ValueError, "k and v must be alike");
         const qbn_kv_batch b = batch(dev, k.t.size(0), tensor(a[4], "table"), tensor(a[5], "lens"), a[6]);
         return PyLong_FromLong(qbn_kv_append(c, integer(a[7]), &b, k.t.data_ptr(), k.token, k.head, v.t.data_ptr(), v.token,
-                                             v.head, t == at::kFloat ? QBN_F32 : QBN_BF16, stream_of(dev)));
+                                             v.head, t == at::kFloat ? QBN_F32 : QBN_BF16, OnDevice(dev)));
     });
 }
 
@@ -208,7 +247,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Workspace w = workspace(a[13], need, dev, q.t);
         const auto f = decode ? qbn_kv_attention_decode : qbn_kv_attention_prefill;
         const int32_t st = f(c, integer(a[10]), &b, heads > INT32_MAX ? -1 : (int32_t)heads, q.t.data_ptr(), q.token, q.head,
-                             (float)scale, window, sinks, out.data_ptr(), (float *)lse.data_ptr(), w.p, w.bytes, stream_of(dev));
+                             (float)scale, window, sinks, out.data_ptr(), (float *)lse.data_ptr(), w.p, w.bytes, OnDevice(dev));
         if (st) return PyLong_FromLong(st);
         PyObject *r = PyTuple_New(2);
         if (!r) return nullptr;
@@ -275,7 +314,7 @@ PyObject *reserve(PyObject *, PyObject *const *a, Py_ssize_t n) {  // in, out, d
         const int32_t *r = ints(rows, count, dev, "rows"), *t = ints(tensor(a[4], "tokens"), count, dev, "tokens");
         at::Tensor status = word(a[5], dev, rows, "status");
         const Workspace w = workspace(a[6], qbn_kv_pool_workspace(in, count), dev, rows);
-        return status_and(qbn_kv_reserve(in, out, count, r, t, (int32_t *)status.data_ptr(), w.p, w.bytes, stream_of(dev)),
+        return status_and(qbn_kv_reserve(in, out, count, r, t, (int32_t *)status.data_ptr(), w.p, w.bytes, OnDevice(dev)),
                           std::move(status));
     });
 }
@@ -291,7 +330,7 @@ PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n) {  // cache, in, ou
         const int32_t *p = ints(parents, count, dev, "parents"), *k = ints(tensor(a[5], "children"), count, dev, "children");
         at::Tensor status = word(a[6], dev, parents, "status");
         const Workspace w = workspace(a[7], qbn_kv_pool_workspace(in, count), dev, parents);
-        return status_and(qbn_kv_fork(c, in, out, count, p, k, (int32_t *)status.data_ptr(), w.p, w.bytes, stream_of(dev)),
+        return status_and(qbn_kv_fork(c, in, out, count, p, k, (int32_t *)status.data_ptr(), w.p, w.bytes, OnDevice(dev)),
                           std::move(status));
     });
 }
@@ -302,7 +341,7 @@ PyObject *release(PyObject *, PyObject *const *a, Py_ssize_t n) {  // in, out, d
         const int64_t dev = integer(a[2]);
         const at::Tensor &rows = tensor(a[3], "rows");
         return PyLong_FromLong(qbn_kv_free(handle<qbn_kv_pool>(a[0]), handle<qbn_kv_pool>(a[1]), rows.numel(),
-                                           ints(rows, rows.numel(), dev, "rows"), int32(a[4]), int32(a[5]), stream_of(dev)));
+                                           ints(rows, rows.numel(), dev, "rows"), int32(a[4]), int32(a[5]), OnDevice(dev)));
     });
 }
 
@@ -315,7 +354,7 @@ PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {  // cache, in,
         at::Tensor live = word(a[5], dev, like, "live");
         const Workspace w = workspace(a[6], qbn_kv_pool_workspace(in, 0), dev, like);
         return status_and(qbn_kv_compact(handle<qbn_kv_cache>(a[0]), in, handle<qbn_kv_pool>(a[2]), (int32_t *)live.data_ptr(),
-                                         w.p, w.bytes, stream_of(dev)),
+                                         w.p, w.bytes, OnDevice(dev)),
                           std::move(live));
     });
 }
@@ -334,6 +373,8 @@ PyMODINIT_FUNC PyInit__kvcall() {
     PyObject *c = PyImport_ImportModule("torch._C");
     if (!c) return nullptr;
     g_raw_stream = PyObject_GetAttrString(c, "_cuda_getCurrentRawStream");
+    g_exchange = PyObject_GetAttrString(c, "_cuda_exchangeDevice");
+    g_exchange_back = PyObject_GetAttrString(c, "_cuda_maybeExchangeDevice");
     Py_DECREF(c);
-    return g_raw_stream ? PyModule_Create(&g_module) : nullptr;
+    return g_raw_stream && g_exchange && g_exchange_back ? PyModule_Create(&g_module) : nullptr;
 }
