@@ -124,7 +124,8 @@ int32_t check_attention(const qbn_kv_cache *c, int64_t layer, const qbn_kv_batch
     int32_t st = check_batch(c, layer, b);
     if (st) return st;
     if (q_heads <= 0 || q_heads % c->heads || q_heads > (1 << 16)) return QBN_ERR_SHAPE;
-    if (window < 0 || sinks < 0 || window > kMaxTokens || sinks > kMaxTokens || !isfinite(scale)) return QBN_ERR_SHAPE;
+    if (window < 0 || sinks < 0 || window > kMaxTokens || sinks > kMaxTokens) return QBN_ERR_SHAPE;
+    if (!isfinite(scale * (float)M_LOG2E)) return QBN_ERR_SHAPE;  // the kernels' factor
     if (b->tokens == 0) return QBN_OK;
     if (b->tokens > kMaxTokens / q_heads) return QBN_ERR_SHAPE;
     st = check_rows(q, qt, qh, b->tokens, q_heads, 2);

@@ -118,7 +118,7 @@ QBN_API int32_t qbn_kv_append(const qbn_kv_cache *cache, int64_t layer, const qb
  * ascend or leaves 0 .. tokens, all outputs are NaN.
  * q: QBN_BF16 with strides as in qbn_kv_append; out: bfloat16
  * [tokens][q_heads][head_dim], lse: binary32 [tokens][q_heads] or NULL.
- * q_heads % heads == 0. Products are exact, sums, softmax statistics and
+ * q_heads % heads == 0; scale * log2 e is finite. Products are exact, sums, softmax statistics and
  * accumulators binary32; the softmax weights are rounded to bfloat16 for the
  * product with V (relative 2^-9 each, below the output's own rounding), their
  * sum is not. No atomics: repeated calls give bit-identical results.

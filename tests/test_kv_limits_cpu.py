@@ -10,13 +10,13 @@ A = 0x10000
 SHAPE = 4
 
 
-def call(decode, seqs, tokens, heads, q_heads, row, cu=None):
+def call(decode, seqs, tokens, heads, q_heads, row, cu=None, scale=0.1):
     lib = kv._kv()
     c = ctypes.byref(kv._CCache(16, heads, 64, 16, 1, 8, A, A, None, None))
     b = ctypes.byref(kv._CBatch(seqs, tokens, row, row, A, A, cu))
     f = lib.qbn_kv_attention_decode if decode else lib.qbn_kv_attention_prefill
     got = lib.qbn_kv_attention_workspace(c, b, q_heads, 0, 0, int(decode))
-    return got, f(c, 0, b, q_heads, A, 64 * q_heads, 64, 0.1, 0, 0, A, A, A, 1 << 60, None)
+    return got, f(c, 0, b, q_heads, A, 64 * q_heads, 64, scale, 0, 0, A, A, A, 1 << 60, None)
 
 
 @pytest.mark.parametrize("decode,seqs,heads,q_heads,row", [
@@ -40,3 +40,13 @@ def test_the_most_sequences_fit(decode):
     c = ctypes.byref(kv._CCache(16, 8, 64, 16, 1, 8, A, A, None, None))
     b = ctypes.byref(kv._CBatch(1 << 20, 1 << 20, 4096, 4096, A, A, None))
     assert kv._kv().qbn_kv_attention_workspace(c, b, 32, 0, 0, int(decode)) >= 0
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_scales_that_pass_binary32_in_base_2_are_refused(decode, scale):
+    """scale * log2 e would be infinite, and 0 times it NaN. (Without tokens there
+    is nothing to launch.)"""
+    assert call(decode, 4, 4, 2, 4, 1, scale=scale)[1] == SHAPE
+    assert call(decode, 0, 0, 2, 4, 1, scale=scale)[1] == SHAPE
+    assert call(decode, 0, 0, 2, 4, 1, scale=2.3e38)[1] == 0
