@@ -369,7 +369,7 @@ struct Decoder {
             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(column8<W>(c, t)), p, acc[t], 0, 0, 0);
     }
 
-    __device__ __forceinline__ void step(const T &tile, int t0, const bf16x8 *q, float &ref, float &sum, f32x4 *acc) {
+    __device__ __forceinline__ void step(const T &tile, int t0, const bf16x8 *q, float &ref, bool &far, float &sum, f32x4 *acc) {
         // whole tiles that every query head sees need no mask
         const bool whole = t0 + 31 < sp.len && (t0 >= sp.lo || t0 + 31 < a.sinks);
         Parts r;
@@ -407,11 +407,18 @@ struct Decoder {
             const float now = __builtin_fmaxf(ref, top);
             const float f = now == ref ? 1.0f : exp2_fast(ref - now);
             ref = now;
+            far = __any(__builtin_fabsf(ref) >= kFar && ref != kNegInf);
             sum *= f;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) acc[t] *= f;
         }
-        const float base = ref == kNegInf ? 0.0f : ref;
+        float base = ref == kNegInf ? 0.0f : ref;
+        if (far) {
+            const float inv = 1.0f / a.scale;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = brought_near(x[j], a.scale, base, inv);
+            base = 0.0f;
+        }
         u32x4 p;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -501,6 +508,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) acc[t] = f32x4{0, 0, 0, 0};
     float ref = kNegInf, sum = 0.0f;
+    bool far = false;  // some row's reference is
     T cur, nxt;
     const auto token = [&](int u) { return w.unit_token(u) + 32 * wave; };
     // Two tiles in turn, the next one's loads in flight: issued before the step,
@@ -512,7 +520,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
         __builtin_amdgcn_sched_barrier(0);
     };
     const auto step = [&](const T &r, int u) {
-        w.step(r, token(u), q, ref, sum, acc);
+        w.step(r, token(u), q, ref, far, sum, acc);
         __builtin_amdgcn_sched_barrier(0);
     };
     if (u0 < u1) {

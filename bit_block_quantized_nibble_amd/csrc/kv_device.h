@@ -177,6 +177,18 @@ __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast
 // largest.
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The exponent of a weight is fma(x, scale, -base), base being the running
+// reference rounded to binary32. What it was rounded by is common to all
+// weights of a row and falls out of their quotient, but from 2^27 on it is more
+// than 4, and soon all weights are 0 or infinite. Scores so large are brought
+// to the reference first, each product rounded: x' with x' scale = fl(x scale) - base.
+constexpr float kFar = 134217728.0f;
+__device__ __forceinline__ float brought_near(float x, float scale, float base, float inv_scale) {
+#pragma clang fp contract(off)
+    const float y = x * scale;
+    return (y - base) * inv_scale;
+}
+
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ int dpp_i32(int v) {
     return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);

@@ -380,7 +380,10 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     const auto larger = [&](const Scores &x, float top, int i) {
         return here(__builtin_fmaxf(top, __builtin_fmaxf(x.s[i / 8][2 * i % 16], x.s[i / 8][2 * i % 16 + 1])));
     };
-    // Masks the scores of an edge and raises the reference where they exceed it.
+    // Masks the scores of an edge and raises the reference where they exceed it;
+    // `base` is what their weights' exponents are taken from.
+    float base = 0.0f;
+    bool far = false;
     const auto settle = [&](Scores &x, float top, int t0, bool edge) {
         if (edge) {
             top = kNegInf;
@@ -400,9 +403,19 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             const float now = __builtin_fmaxf(ref, top);
             const float f = now == ref ? 1.0f : exp2_fast(ref - now);
             ref = now;
+            far = __any(__builtin_fabsf(ref) >= kFar && ref != kNegInf);
             sum *= f;
 #pragma unroll
             for (int t = 0; t < D / 32; ++t) acc[t] *= f;
+        }
+        base = ref == kNegInf ? 0.0f : ref;
+        if (far) {
+            const float inv = 1.0f / a.scale;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x.s[t][e] = brought_near(x.s[t][e], a.scale, base, inv);
+            base = 0.0f;
         }
     };
     if (tid == 0) s_odd = s_bad = 0;
@@ -467,7 +480,6 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) asm volatile("" : "+a"(q[k]));
             }
-            const float base = ref == kNegInf ? 0.0f : ref;
             Weights w;
             bf16x8 part[AHEAD];
 #pragma unroll
@@ -507,7 +519,6 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             __syncthreads();
         };
         const auto last = [&](int buf, Scores &x) {
-            const float base = ref == kNegInf ? 0.0f : ref;
             Weights w;
 #pragma unroll
             for (int k = 0; k < TICKS; ++k) tick(x, base, w, k);
