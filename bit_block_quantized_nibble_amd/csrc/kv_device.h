@@ -32,8 +32,8 @@ struct Batch {
 
 // The scale operand of the converts for E8M0 byte `j` of w. They take its
 // exponent bits, so the byte in their place serves for all 256 values (0 stands
-// for 2^-127 there, 255 gives NaN; every byte with every code was compared
-// with the value 2^(b - 127) as the operand).
+// for 2^-127 there, 255 gives NaN; tests pass every byte with every code through
+// both attention kernels).
 __device__ __forceinline__ float e8m0_operand(uint32_t w, int j = 0) {
     return __uint_as_float(((w >> (8 * j)) & 0xFFu) << 23);
 }
@@ -78,8 +78,9 @@ __device__ __forceinline__ int count_upto(const int32_t *list, int n, int v) {
     return min(at, n);
 }
 
-// Eight consecutive elements (4, 8 or 16 bytes in w) -> bf16 pairs, exact: an
-// E2M1 or E4M3FN value has at most 4 significant bits.
+// Eight consecutive elements (4, 8 or 16 bytes in w) -> bf16 pairs: exact, an
+// E2M1 or E4M3FN value having at most 4 significant bits, where the exponent fits
+// (E4M3 from scale byte 3 to 246, E2M1 up to 252); beyond, rounded to nearest or infinite.
 template <int F>
 __device__ __forceinline__ void expand8(const uint32_t *w, float scale, uint32_t (&o)[4]) {
     if constexpr (F == FP4) {

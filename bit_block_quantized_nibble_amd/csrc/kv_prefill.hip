@@ -360,7 +360,10 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     };
     // Word k of the weights is made of scores 2k and 2k + 1, in three ticks, so
     // that nothing waits for the exponential before it: tick k scales the
-    // scores, tick k + 1 takes the powers, tick k + 2 adds and rounds.
+    // scores, tick k + 1 takes the powers, tick k + 2 adds and rounds: to
+    // bfloat16 for the product with V (2^-8 of a weight at most; an output is off
+    // from binary64 by 1.1 to 1.4 times as much as with binary32 weights, which
+    // would need two products in place of one), while the sum takes them as they are.
     float arg[2][2], pow[2][2];
     const auto tick = [&](const Scores &x, float base, Weights &w, int k) {
         if (k >= 1 && k <= 16) {

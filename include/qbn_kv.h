@@ -111,6 +111,9 @@ QBN_API int32_t qbn_kv_append(const qbn_kv_cache *cache, int64_t layer, const qb
  * j > p - window, or j < sinks): the last `window` tokens up to p itself, and
  * the first `sinks` ones. A query that sees nothing (lens[b] == 0, more new
  * tokens than lens[b], or a row of no sequence) gives out = 0, lse = -inf.
+ * So does one whose visible scores are all -inf (no softmax of theirs exists);
+ * a visible score of +inf or NaN gives NaN in out and lse, and an infinity of a
+ * visible v_j whose weight is below binary32 gives an infinity or NaN.
  * What is stored in tokens that a query does not see, infinities and NaN
  * included, never reaches its output. If a visible token's table entry is not
  * a page of the cache, or lens[b] is negative or beyond the row, the outputs
@@ -118,10 +121,16 @@ QBN_API int32_t qbn_kv_append(const qbn_kv_cache *cache, int64_t layer, const qb
  * ascend or leaves 0 .. tokens, all outputs are NaN.
  * q: QBN_BF16 with strides as in qbn_kv_append; out: bfloat16
  * [tokens][q_heads][head_dim], lse: binary32 [tokens][q_heads] or NULL.
- * q_heads % heads == 0; scale * log2 e is finite. Products are exact, sums, softmax statistics and
- * accumulators binary32; the softmax weights are rounded to bfloat16 for the
- * product with V (relative 2^-9 each, below the output's own rounding), their
- * sum is not. No atomics: repeated calls give bit-identical results.
+ * q_heads % heads == 0; scale * log2 e is finite.
+ * Elements times their scales enter as bfloat16, which holds them exactly but
+ * for two ends: E4M3 values with scale bytes 0 to 2 may lie below its smallest
+ * (rounded to nearest), and E4M3 with bytes from 247 and E2M1 with bytes from
+ * 253 on may pass its largest (infinite). qbn_kv_append writes those bytes only
+ * for magnitudes below 2^-116, and for infinities. Products are exact; sums,
+ * softmax statistics and accumulators are binary32. The softmax weights are
+ * rounded to bfloat16 for the product with V (by 2^-8 of each at most, as much
+ * as the output's own rounding), their sum is not. No atomics: repeated calls
+ * give bit-identical results.
  * The work is split over a sequence's length where there are few sequences;
  * the pieces go through `workspace` (device, 16-byte aligned, at least
  * qbn_kv_attention_workspace bytes, not kept: it may be shared by calls that
