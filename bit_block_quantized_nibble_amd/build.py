@@ -4,7 +4,9 @@ Each .hip source under csrc/ is compiled to an object in _build/ (in
 parallel), then linked into bit_block_quantized_nibble_amd/libqbn.so, next
 to this file, so that the built library travels with the source tree. Next to
 it, _kvcall.so: the Python module that makes the paged cache's calls (host
-code, built against torch's headers and linked to libqbn.so).
+code, built with g++ against Python's and torch's headers and linked to
+libqbn.so). Where that one cannot be built, the library is all the same, and
+everything but the paged cache's Python calls runs; the error comes last.
 
     python -m bit_block_quantized_nibble_amd.build
 """
@@ -75,14 +77,18 @@ def build(verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(jobs) as ex:
         calls = ex.submit(_compile_calls)
         objs = list(ex.map(_compile, srcs))
-        calls = calls.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-fno-gpu-rdc", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("hipcc link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    _link_calls(calls)
+    try:
+        _link_calls(calls.result())
+    except Exception as e:
+        if os.path.exists(CALLS):  # of another build: it may not fit this library
+            os.remove(CALLS)
+        raise RuntimeError("%s is built, but not %s, which makes the paged cache's Python calls" % (LIB, CALLS)) from e
     if verbose:
         print("built", LIB, CALLS)
     return LIB
