@@ -9,14 +9,17 @@
 //
 // Bound by latency for a decode step and by HBM for prompts: every element
 // is read once and written once. A wave takes 512 elements of K or V of one
-// token, or of four where there are many, eight per lane and token, so that a lane's load is 16 bytes (bf16) and its
-// store 4 (E2M1), 8 (E4M3) or 16; four lanes share a block's maximum by
+// token, or of four where there are many, eight per lane and token, so that a
+// lane's load is 16 bytes (bf16) and its store 4 (E2M1), 8 (E4M3) or 16; four lanes share a block's maximum by
 // quad permutes. The token's sequence is found by one ballot, of more than 64
 // by a search with 64 samples a step.
 //
-// Measured: 16 tokens of 8 heads of 128 to MXFP8 3.4 us; prompts of 4789
-// tokens in all, bf16 to MXFP4, 9.3 us (8.3 where the same pages are written
-// over and over), of 65536 70 us (4.8 TB/s; a copy of 2 GiB reaches 4.95).
+// Measured, 8 heads of 128: 16 tokens to MXFP8 3.4 us; 4789 tokens in four
+// prompts, bf16 to bf16, MXFP8 and MXFP4 9.0, 9.5 and 8.9 us; 16384 26.9, 26.7
+// and 21.5; 65536 100, 82 and 73 (4.7 to 5.4 TB/s; a copy of 2 GiB reaches
+// 4.95). That is 3 us for the chain of launch, cu, length, table and store, and
+// then the bytes (MXFP4 1.07 us for 1024 tokens, its floor), so that a few
+// thousand tokens take nearly twice their floor.
 #include "kv_device.h"
 #include "kv_launch.h"
 

@@ -36,11 +36,11 @@
 // page table, first tile and output, and that chain is most of a short call.)
 //
 // Measured (kernel and join, one layer): 32 sequences of up to 4096 tokens, 8
-// heads of 128, MXFP8 (100 MB): 23.0 + 3.9 us, 4.3 TB/s in the first; two of
-// up to 131072 tokens, MXFP4 (179 MB): 37.0 + 4.8 us, 4.8 TB/s, nearly what
-// a copy of 2 GiB reaches (4.95); 64 with a window of 4096 and one head of 64,
-// MXFP4 (15 MB): 10.7 + 4.2 us, of which 4 are the chain of launch, lengths, table, first tile
-// and output, and the rest is instruction issue. Tried and slower: three or four
+// heads of 128, MXFP8 (100 MB): 23.1 + 4.2 us, 4.3 TB/s in the first; two of
+// up to 131072 tokens, MXFP4 (179 MB): 36.8 + 4.7 us, 4.9 TB/s, what a copy of
+// 2 GiB reaches (4.95); 64 with a window of 4096 and one head of 64, MXFP4
+// (15 MB): 10.6 + 4.1 us, of which 4 are the chain of launch, lengths, table,
+// first tile and output, and the rest is instruction issue. Tried and slower: three or four
 // tiles in flight (batch 28.9 -> 32.6 us), 1024 pieces instead of 512 (long
 // 37.4 -> 39.7), and the join inside this kernel by the workgroup that
 // finishes last (long 41.4 -> 46.4, though window 12.8 -> 11.8).
@@ -175,10 +175,12 @@ __global__ __launch_bounds__(kPlanThreads) void k_decode_plan(DecodeArgs a) {
 }
 
 // A wave's 32 tokens as loaded. A vector memory instruction takes a compute
-// unit's address unit 16 cycles whatever its width, so all loads but those of
-// a page entry are 16 bytes a lane where they can be: K's pieces are, V's and
-// the scales go through LDS (the wave's own part, no barrier), where the
-// narrow pieces that the matrix operands are made of cost a quarter.
+// unit's address unit 16 cycles whatever its width, so loads are 16 bytes a lane
+// where they can be: V and the scales go through LDS (the wave's own part, no
+// barrier), where the narrow pieces that the matrix operands are made of cost
+// a quarter. K's pieces are 16 bytes, but 8 (MXFP4 at 64 and 192, MXFP8 at 96)
+// or 4 (MXFP4 at 96) where the row has no more for a lane group: 32 sequences
+// of 4096 tokens, MXFP4, 3.1 TB/s at 64 and 96 against 4.3 at 128.
 template <int F, int D>
 struct Tile {
     static constexpr int ROW = D * kBits<F> / 8;  // bytes of a token's head

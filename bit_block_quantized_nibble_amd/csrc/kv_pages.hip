@@ -305,8 +305,9 @@ __global__ __launch_bounds__(256) void k_free(Pool p, int count, const int32_t *
 }
 
 // Both in one workgroup, for tables that it passes over faster than two kernels
-// start (2.7 us for 800 entries against 4.8, but 11.5 for 15000 against 9.3):
-// out = in without the pages of the rows named.
+// start: out = in without the pages of the rows named. In one and in two, us:
+// 800 entries 2.5 and 4.3, 2040 3.0 and 4.4, 3000 3.5 and 4.4, 4100 4.6 and 4.5,
+// 8000 6.5 and 4.4, 15000 10.7 and 4.5.
 constexpr int64_t kFreeTable = 4096, kFreePages = 4096;
 constexpr int kFreeSlots = 4096;
 __global__ __launch_bounds__(kThreads) void k_copy_free(Pool in, Pool out, int count, const int32_t *rows, int window, int sinks) {

@@ -18,12 +18,14 @@
 // exceeds the running reference by 2^8.
 //
 // Bound by the matrix cores together with the vector instructions: a wave's
-// tile of 32 rows and 64 tokens (head_dim 128) is 32 products of 33.5 cycles
-// and about 200 vector instructions of 4.5, two waves share a SIMD, and under
-// this load the clock is near 2.0 GHz. Measured: a prompt of 4096 tokens, 32
-// query and 8 key-value heads of 128, bf16 cache: 143 us, 960 TFLOP/s of
+// tile of 32 rows and 64 tokens (head_dim 128) is 32 products of 32 cycles
+// and 206 vector instructions, two waves share a SIMD, and under this load the
+// clock is near 2.0 GHz. Of the time the matrix cores are busy 40 %, the vector
+// units 38 % and LDS 30 %; one compute unit in seven waits for the last row
+// tiles. Measured: a prompt of 4096 tokens, 32 query and 8 key-value heads of
+// 128, bf16 cache: 147 to 155 us from card to card, 890 to 935 TFLOP/s of
 // causal products (the library's product of 8192^3 reaches 1327); 8192 new
-// tokens of 16384 with a window of 2048, MXFP4: 306 us, 900 TFLOP/s. Tried and
+// tokens of 16384 with a window of 2048, MXFP4: 304 to 319 us. Tried and
 // slower or equal: 64 rows a wave (199 and 392 us: copies to and from the
 // accumulation registers), raised wave priority in either product, operands
 // read 3 or 6 steps ahead, the barrier inside the second product, four of the
@@ -658,9 +660,13 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
     }
     const int64_t blocks = p.tiles * c.heads;
     // Few row tiles: the length is split until about one workgroup per compute
-    // unit runs, each with at least two tiles of 64 tokens. (72 workgroups of
-    // up to 24 tiles, head_dim 96: in 3 pieces 26.0 us with the join, in 2
-    // 29.0, in 4 28.8, in 6 27.4, whole 35.7.)
+    // unit runs, each with at least two tiles of 64 tokens. For about 128, 256,
+    // 512 and 1024 workgroups, us with the join: chunks of up to 341 tokens on
+    // 1531, 12 / 4 heads of 96 MXFP8 37, 25, 27, 32; 4 of 64 on 2048, 32 / 8 of
+    // 128 bf16 60, 40, 34, 41; 128 and 16 on 8192 and 200, 8 / 1 of 64 MXFP4
+    // 22, 20, 24, 31; 3 of 500 on 1000, 8 / 4 of 256 52, 44, 56, 82; but 256 on
+    // 30000, 32 / 8 of 128 MXFP8 624, 223, 161, 174, and 16 of 16 on 4096, MXFP4
+    // 96, 96, 75, 60.
     int64_t splits = blocks > 0 && blocks < 256 ? 256 / blocks : 1;
     if (splits > units / 2) splits = units / 2;
     p.splits = (int)(splits < 1 ? 1 : splits > 64 ? 64 : splits);

@@ -191,3 +191,24 @@ def test_calls_grow_with_the_sequences_not_with_their_square():
     few, many = times(8192), times(65536)
     for name, a, b in zip(("append", "decode", "prefill"), few, many):
         assert b <= 12 * a, "%s: %.3f ms for 8192 sequences, %.3f for 65536" % (name, a, b)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_empty_batches(fmt):
+    """No sequences, or no rows: nothing is written, the outputs are empty."""
+    c = random_cache(fmt, 2, 1, 16, 64, None, junk=0x5A)
+    before = [t.clone() for t in (c.k, c.v, c.k_scales, c.v_scales) if t is not None]
+    x = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    none, some = torch.zeros(0, 3, dtype=torch.int32, device=DEV), torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    say("empty", fmt)
+    for table, lens, cu in ((none, ints([]), None), (none, ints([]), ints([0])), (some, ints([5, 0]), ints([0, 0, 0]))):
+        qbn.kv_append(c, x, x, table, lens, cu)
+        got = [qbn.kv_attention_prefill(c, q, cu, table, lens)]
+        if cu is None:
+            got.append(qbn.kv_attention_decode(c, q, table, lens))
+        for out, lse in got:
+            assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    torch.cuda.synchronize()
+    for t, was in zip([t for t in (c.k, c.v, c.k_scales, c.v_scales) if t is not None], before):
+        assert torch.equal(t.view(torch.uint8), was.view(torch.uint8))
