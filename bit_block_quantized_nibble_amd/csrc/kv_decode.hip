@@ -65,6 +65,7 @@ struct DecodeArgs {
     int2 *found;   // per pair: its first piece, how many there are
     int32_t *first;  // of more than kScanned sequences [seqs + 1]: pieces (of a pair) of those before
     float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
+    float far_unit;  // the power of two at or below `scale`
     uint32_t q_keep, q_flip;
     int group, tiles, rows;  // query heads per key-value head, 16-row tiles of them, pairs per sequence
     int window, sinks, blocks, dim;
@@ -371,7 +372,7 @@ struct Decoder {
             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(column8<W>(c, t)), p, acc[t], 0, 0, 0);
     }
 
-    __device__ __forceinline__ void step(const T &tile, int t0, const bf16x8 *q, float &ref, bool &far, float &sum, f32x4 *acc) {
+    __device__ __forceinline__ void step(const T &tile, int t0, const bf16x8 *q, Reference &ref, float &sum, f32x4 *acc) {
         // whole tiles that every query head sees need no mask
         const bool whole = t0 + 31 < sp.len && (t0 >= sp.lo || t0 + 31 < a.sinks);
         Parts r;
@@ -402,25 +403,15 @@ struct Decoder {
         float top = x[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[j]);
-        top *= a.scale;
-        if (__any(top > ref + 8.0f)) {
+        if (__any(top * ref.unit > ref.at + 8.0f)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 16));
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-            const float now = __builtin_fmaxf(ref, top);
-            const float f = now == ref ? 1.0f : exp2_fast(ref - now);
-            ref = now;
-            far = __any(__builtin_fabsf(ref) >= kFar && ref != kNegInf);
+            const float f = raise(ref, top, a.scale, a.far_unit);
             sum *= f;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) acc[t] *= f;
         }
-        float base = ref == kNegInf ? 0.0f : ref;
-        if (far) {
-            const float inv = 1.0f / a.scale;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = brought_near(x[j], a.scale, base, inv);
-            base = 0.0f;
-        }
+        const float base = ref.at == kNegInf ? 0.0f : ref.at;
         // The weights enter the product with V as bfloat16, off by 2^-8 of each at
         // most; the sum takes them as they are. Against binary64 an output is then
         // off by 1.1 to 1.4 times as much as with binary32 weights, its own rounding
@@ -428,8 +419,8 @@ struct Decoder {
         u32x4 p;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            const float p0 = exp2_fast(__builtin_fmaf(x[j], a.scale, -base));
-            const float p1 = exp2_fast(__builtin_fmaf(x[j + 1], a.scale, -base));
+            const float p0 = exp2_fast(__builtin_fmaf(x[j], ref.unit, -base));
+            const float p1 = exp2_fast(__builtin_fmaf(x[j + 1], ref.unit, -base));
             sum += p0 + p1;
             p[j / 2] = pack2(p0, p1);
         }
@@ -513,8 +504,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
     f32x4 acc[D / 16];
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) acc[t] = f32x4{0, 0, 0, 0};
-    float ref = kNegInf, sum = 0.0f;
-    bool far = false;  // some row's reference is
+    Reference running = {kNegInf, a.scale};
+    float sum = 0.0f;
     T cur, nxt;
     const auto token = [&](int u) { return w.unit_token(u) + 32 * wave; };
     // Two tiles in turn, the next one's loads in flight: issued before the step,
@@ -526,7 +517,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
         __builtin_amdgcn_sched_barrier(0);
     };
     const auto step = [&](const T &r, int u) {
-        w.step(r, token(u), q, ref, far, sum, acc);
+        w.step(r, token(u), q, running, sum, acc);
         __builtin_amdgcn_sched_barrier(0);
     };
     if (u0 < u1) {
@@ -550,6 +541,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_decode(DecodeArgs a) 
         }
     }
     // ---- the four waves' sums meet in LDS
+    const float ref = scaled(running, a.scale);
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
     if (w.bad || w.sp.bad) sum = __builtin_nanf("");
@@ -762,6 +754,7 @@ hipError_t launch_kv_decode(const qbn_kv_cache &c, int64_t layer, const qbn_kv_b
     a.found = p.blocks ? (int2 *)(a.parts + most_pieces(p) * (16 * c.head_dim + 32)) : nullptr;
     a.first = p.blocks && b.seqs > kScanned ? (int32_t *)((uint8_t *)ws + piece_bytes(p, c.head_dim)) : nullptr;
     a.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
+    a.far_unit = ldexpf(1.0f, ilogbf(a.scale));
     a.q_keep = scale == 0.0f ? 0u : ~0u;
     a.q_flip = scale < 0.0f ? 0x80008000u : 0u;
     a.group = q_heads / c.heads, a.tiles = p.tiles, a.rows = c.heads * p.tiles;

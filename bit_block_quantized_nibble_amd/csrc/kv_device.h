@@ -178,16 +178,31 @@ __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast
 // largest.
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The exponent of a weight is fma(x, scale, -base), base being the running
-// reference rounded to binary32. What it was rounded by is common to all
-// weights of a row and falls out of their quotient, but from 2^27 on it is more
-// than 4, and soon all weights are 0 or infinite. Scores so large are brought
-// to the reference first, each product rounded: x' with x' scale = fl(x scale) - base.
-constexpr float kFar = 134217728.0f;
-__device__ __forceinline__ float brought_near(float x, float scale, float base, float inv_scale) {
-#pragma clang fp contract(off)
-    const float y = x * scale;
-    return (y - base) * inv_scale;
+// A row's running reference and the unit that its scores are taken in. A
+// weight's exponent is fma(x, unit, -ref), ref being a product x unit rounded to
+// binary32. What it was rounded by is common to all weights of a row and falls
+// out of their quotient, but from 2^31 on it passes 64, and soon all weights
+// would be 0 or infinite. There the unit is the power of two below the scale,
+// whose products are exact: two scores so far out that differ at all differ by
+// 128 or more, and by 64 in that unit, so that only the largest has a weight in
+// either. (Rounding all products before the difference, in a branch, cost the
+// prefill kernel 1 to 5 %.)
+constexpr float kFar = 2147483648.0f;
+struct Reference {
+    float at, unit;
+};
+// Raises r to the score `top` if that is larger; the factor of what is summed.
+__device__ __forceinline__ float raise(Reference &r, float top, float scale, float far_unit) {
+    if (!(top * r.unit > r.at)) return 1.0f;
+    const float unit = __builtin_fabsf(top * scale) >= kFar ? far_unit : scale, now = top * unit;
+    const float f = unit == r.unit ? exp2_fast(r.at - now) : 0.0f;
+    r.at = now;
+    r.unit = unit;
+    return f;
+}
+// The reference as a score times the scale.
+__device__ __forceinline__ float scaled(const Reference &r, float scale) {
+    return r.unit == scale ? r.at : r.at * (scale / r.unit);
 }
 
 template <int CTRL, int ROWS = 0xF>

@@ -50,6 +50,7 @@ struct PrefillArgs {
     int32_t *first;  // of more than kScanned sequences with cu [seqs + 1]: row tiles of those before; then, whether cu is out of order
     float *parts;  // [splits][tokens][heads][D] sums, then [splits][tokens][heads] references and weight sums
     float scale;   // |scale| times log2 e; q's sign bits are flipped where it is negative, and q is 0 where it is 0
+    float far_unit;  // the power of two at or below `scale`
     uint32_t q_keep, q_flip;
     int group, window, sinks, splits, dim;
 };
@@ -237,7 +238,8 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
     f32x16 acc[D / 32];
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) acc[t] = f32x16{};
-    float ref = kNegInf, sum = 0.0f;
+    Reference running = {kNegInf, a.scale};
+    float sum = 0.0f;
 
     // Conditions without short circuits: as branches they cost more than they save.
     const auto tile_token = [&](int u) { return (u < sink_tiles ? u : u - sink_tiles + first) * BN; };
@@ -379,16 +381,13 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         }
         if (k < 16) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) arg[k % 2][i] = here(__builtin_fmaf(x.s[k / 8][2 * k % 16 + i], a.scale, -base));
+            for (int i = 0; i < 2; ++i) arg[k % 2][i] = here(__builtin_fmaf(x.s[k / 8][2 * k % 16 + i], running.unit, -base));
         }
     };
     const auto larger = [&](const Scores &x, float top, int i) {
         return here(__builtin_fmaxf(top, __builtin_fmaxf(x.s[i / 8][2 * i % 16], x.s[i / 8][2 * i % 16 + 1])));
     };
-    // Masks the scores of an edge and raises the reference where they exceed it;
-    // `base` is what their weights' exponents are taken from.
-    float base = 0.0f;
-    bool far = false;
+    // Masks the scores of an edge and raises the reference where they exceed it.
     const auto settle = [&](Scores &x, float top, int t0, bool edge) {
         if (edge) {
             top = kNegInf;
@@ -402,25 +401,12 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
                     top = __builtin_fmaxf(top, x.s[t][e]);
                 }
         }
-        top *= a.scale;
-        if (__any(top > ref + 8.0f)) {
+        if (__any(top * running.unit > running.at + 8.0f)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-            const float now = __builtin_fmaxf(ref, top);
-            const float f = now == ref ? 1.0f : exp2_fast(ref - now);
-            ref = now;
-            far = __any(__builtin_fabsf(ref) >= kFar && ref != kNegInf);
+            const float f = raise(running, top, a.scale, a.far_unit);
             sum *= f;
 #pragma unroll
             for (int t = 0; t < D / 32; ++t) acc[t] *= f;
-        }
-        base = ref == kNegInf ? 0.0f : ref;
-        if (far) {
-            const float inv = 1.0f / a.scale;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x.s[t][e] = brought_near(x.s[t][e], a.scale, base, inv);
-            base = 0.0f;
         }
     };
     if (tid == 0) s_odd = s_bad = 0;
@@ -485,6 +471,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) asm volatile("" : "+a"(q[k]));
             }
+            const float base = running.at == kNegInf ? 0.0f : running.at;
             Weights w;
             bf16x8 part[AHEAD];
 #pragma unroll
@@ -524,6 +511,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             __syncthreads();
         };
         const auto last = [&](int buf, Scores &x) {
+            const float base = running.at == kNegInf ? 0.0f : running.at;
             Weights w;
 #pragma unroll
             for (int k = 0; k < TICKS; ++k) tick(x, base, w, k);
@@ -543,6 +531,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
         }
     }
 
+    const float ref = scaled(running, a.scale);
     sum += __shfl_xor(sum, 32);
     if (bad || s_bad) sum = __builtin_nanf("");
     const int64_t total = (int64_t)a.b.tokens * (a.c.heads * a.group), shift = total * blockIdx.y;
@@ -726,6 +715,7 @@ hipError_t launch_kv_prefill(const qbn_kv_cache &c, int64_t layer, const qbn_kv_
     a.parts = (float *)ws;
     a.first = listed(b) ? (int32_t *)((uint8_t *)ws + part_bytes(p, c, b, q_heads)) : nullptr;
     a.scale = scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
+    a.far_unit = ldexpf(1.0f, ilogbf(a.scale));
     a.q_keep = scale == 0.0f ? 0u : ~0u;
     a.q_flip = scale < 0.0f ? 0x80008000u : 0u;
     a.group = q_heads / c.heads, a.window = window, a.sinks = sinks, a.splits = p.splits, a.dim = c.head_dim;
