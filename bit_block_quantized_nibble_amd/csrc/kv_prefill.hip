@@ -75,14 +75,8 @@ __device__ __forceinline__ T here(T v) {
     return v;
 }
 
-// A sequence's new tokens; -1 where cu is out of order or leaves q.
-__device__ __forceinline__ int new_tokens(const Batch &b, int s, int &first) {
-    if (!b.cu) {
-        first = s;
-        return 1;
-    }
-    const int x = b.cu[s], y = b.cu[s + 1];
-    first = x;
+// A sequence's new tokens, rows x to y of q; -1 where cu is out of order or leaves q.
+__device__ __forceinline__ int new_tokens(const Batch &b, int x, int y) {
     return x >= 0 && y >= x && y <= b.tokens ? y - x : -1;
 }
 
@@ -99,9 +93,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_prefill_plan(PrefillArgs a, in
     bool wrong = false;
     for (int s0 = 0; s0 < a.b.seqs; s0 += kPlanThreads) {
         const int s = s0 + threadIdx.x;
-        int x;
         int64_t all;
-        const int n = s < a.b.seqs ? new_tokens(a.b, s, x) : 0;
+        const int n = s < a.b.seqs ? new_tokens(a.b, a.b.cu[s], a.b.cu[s + 1]) : 0;
         wrong |= n < 0;
         const int64_t at = block_scan<kPlanThreads>(row_tiles(n, a.group, bm), s_scan, all);
         if (s < a.b.seqs) a.first[s] = (int)min(before + at, (int64_t)0x7FFFFFFF);  // beyond the grid: cu is out of order
@@ -177,25 +170,33 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             wrong = a.first[a.b.seqs + 1] != 0;
             b = count_upto(a.first, a.b.seqs, want);
             if (b < a.b.seqs) {
-                fresh = new_tokens(a.b, b, q0);
+                q0 = start_of(a.b, b);
+                fresh = new_tokens(a.b, q0, start_of(a.b, b + 1));
                 tile = (int)row_tiles(fresh, a.group, L::BM) - 1 - (want - a.first[b]);
                 len = length_of(a.b, b);
             }
-        } else {  // each wave scans the sequences for itself, 64 at a time
-            for (int before = 0, s0 = 0; s0 < a.b.seqs; s0 += 64) {
-                const int s = s0 + lane;
-                int x = 0, n = 0, l = 0;
-                if (s < a.b.seqs) n = new_tokens(a.b, s, x), l = a.b.lens[s];
+        } else {  // each wave scans the sequences for itself, 64 at a time, all loads in flight
+            constexpr int CHUNKS = kScanned / 64;
+            int x[CHUNKS], y[CHUNKS], l[CHUNKS], before = 0;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int s = min(64 * i + lane, a.b.seqs - 1);
+                if (i == 0 || 64 * i < a.b.seqs) x[i] = a.b.cu[s], y[i] = a.b.cu[s + 1], l[i] = a.b.lens[s];
+            }
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                if (i > 0 && 64 * i >= a.b.seqs) break;
+                const int n = 64 * i + lane < a.b.seqs ? new_tokens(a.b, x[i], y[i]) : 0;
                 wrong |= __any(n < 0);
                 const int upto = wave_scan((int)row_tiles(n, a.group, L::BM));
                 const uint64_t here = __ballot(want >= before && want < before + upto);
                 if (here) {
                     const int at = __builtin_ctzll(here);
-                    b = s0 + at;
+                    b = 64 * i + at;
                     tile = before + __builtin_amdgcn_readlane(upto, at) - 1 - want;
-                    q0 = __builtin_amdgcn_readlane(x, at);
+                    q0 = __builtin_amdgcn_readlane(x[i], at);
                     fresh = __builtin_amdgcn_readlane(n, at);
-                    len = __builtin_amdgcn_readlane(l, at);
+                    len = __builtin_amdgcn_readlane(l[i], at);
                 }
                 before += __builtin_amdgcn_readlane(upto, 63);
             }
@@ -637,9 +638,12 @@ struct Plan {
 Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int window, int sinks) {
     Plan p;
     const int64_t group = q_heads / c.heads;
-    // Tiles of 256 rows where they fill the compute units and the sequences fill
-    // them (65536 sequences of one row, 4 heads of 64: 6.6 ms, in tiles of 128 rows 3.1).
-    p.waves = c.head_dim <= 128 && b.tokens * group / 256 * c.heads >= 256 && b.tokens * group >= 256 * b.seqs ? 8 : 4;
+    // Tiles of 256 rows where they fill the compute units and a sequence has more
+    // than 128 on the average. Tiles of 256 and of 128, us: MXFP8, 32 / 8 heads of
+    // 128 on 2048 tokens, 160 sequences of 64 rows 344 and 216, 80 of 128 202 and
+    // 133, 64 of 160 142 and 156, 51 of 200 133 and 143, 42 of 240 130 and 119 (of
+    // 64 93 and 74); 65536 of one row, 4 heads of 64, 6.6 ms and 3.1.
+    p.waves = c.head_dim <= 128 && b.tokens * group / 256 * c.heads >= 256 && b.tokens * group > 128 * b.seqs ? 8 : 4;
     const int BM = p.waves * 32;
     p.tiles = b.cu ? b.tokens * group / BM + b.seqs : b.seqs * ((group + BM - 1) / BM);
     int64_t units = (b.row * c.page_size + BN - 1) / BN;

@@ -212,3 +212,45 @@ def test_empty_batches(fmt):
     torch.cuda.synchronize()
     for t, was in zip([t for t in (c.k, c.v, c.k_scales, c.v_scales) if t is not None], before):
         assert torch.equal(t.view(torch.uint8), was.view(torch.uint8))
+
+
+def test_many_sequences_in_a_graph():
+    """A step of more sequences than the waves scan, captured and replayed beside
+    eager calls while lengths and rows change in place."""
+    rng = np.random.default_rng(12)
+    seqs, ps, dim, heads = 300, 16, 64, 2
+    lens = rng.integers(1, 120, seqs)
+    table = R.torch_table([int(n) + 8 for n in lens], ps, 64, 9 * seqs, rng).to(DEV)
+    c = random_cache("mxfp4", 9 * seqs, heads, ps, dim, rng)
+    fill(c, table.cpu(), [int(n) for n in lens], rng)
+    k, v = (torch.zeros(2 * seqs, heads, dim, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q = torch.zeros(2 * seqs, 4 * heads, dim, dtype=torch.bfloat16, device=DEV)
+    n, cu = ints(lens.tolist()), ints((2 * np.arange(seqs + 1)).tolist())
+
+    def step():
+        qbn.kv_append(c, k, v, table, n, cu)
+        return qbn.kv_attention_decode(c, q[:seqs], table, n) + qbn.kv_attention_prefill(c, q, cu, table, n)
+
+    n.add_(2)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for rep in range(4):
+        for t in (q, k, v):
+            t.copy_(vectors(rng, *t.shape))
+        n.add_(1)
+        cu.copy_(ints(np.concatenate([[rep], np.sort(rng.integers(rep, 2 * seqs, seqs - 1)), [2 * seqs - rep]]).tolist()))
+        torch.cuda.synchronize()
+        say("graph replay", rep)
+        g.replay()
+        torch.cuda.synchronize()
+        after = [t.clone() for t in (c.k, c.v, c.k_scales, c.v_scales)]
+        want = step()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+        for x, y in zip(after, (c.k, c.v, c.k_scales, c.v_scales)):
+            assert torch.equal(x, y)
+    del g
