@@ -19,11 +19,11 @@
 //
 // Bound by the matrix cores together with the vector instructions: a wave's
 // tile of 32 rows and 64 tokens (head_dim 128) is 32 products of 32 cycles
-// and 206 vector instructions, two waves share a SIMD, and under this load the
-// clock is near 2.0 GHz. Of the time the matrix cores are busy 40 %, the vector
-// units 38 % and LDS 30 %; one compute unit in seven waits for the last row
+// and 207 vector instructions, two waves share a SIMD, and under this load the
+// clock is near 2.0 GHz. Of the time the matrix cores are busy 42 %, the vector
+// units 39 % and LDS 31 %; one compute unit in seven waits for the last row
 // tiles. Measured: a prompt of 4096 tokens, 32 query and 8 key-value heads of
-// 128, bf16 cache: 147 to 155 us from card to card, 890 to 935 TFLOP/s of
+// 128, bf16 cache: 142 to 156 us from card to card, 880 to 968 TFLOP/s of
 // causal products (the library's product of 8192^3 reaches 1327); 8192 new
 // tokens of 16384 with a window of 2048, MXFP4: 304 to 319 us. Tried and
 // slower or equal: 64 rows a wave (199 and 392 us: copies to and from the
@@ -465,7 +465,7 @@ __global__ __launch_bounds__(NW * 64, D <= 128 ? 2 : 1) void k_prefill(PrefillAr
             // instructions and copies reach holds what only matrix instructions
             // use. Left to itself the compiler puts the scores there and stores
             // others to memory (4096 tokens, 32 / 8 heads, bf16: 256 wide 599 us,
-            // so 345; 192 wide 285, so 278).
+            // so 349; 192 wide 285, so 272).
             if constexpr (D > 128) {
 #pragma unroll
                 for (int t = 0; t < D / 32; ++t) asm volatile("" : "+a"(acc[t]));
@@ -655,11 +655,11 @@ Plan plan_of(const qbn_kv_cache &c, const qbn_kv_batch &b, int q_heads, int wind
     // Few row tiles: the length is split until about one workgroup per compute
     // unit runs, each with at least two tiles of 64 tokens. For about 128, 256,
     // 512 and 1024 workgroups, us with the join: chunks of up to 341 tokens on
-    // 1531, 12 / 4 heads of 96 MXFP8 37, 25, 27, 32; 4 of 64 on 2048, 32 / 8 of
-    // 128 bf16 60, 40, 34, 41; 128 and 16 on 8192 and 200, 8 / 1 of 64 MXFP4
-    // 22, 20, 24, 31; 3 of 500 on 1000, 8 / 4 of 256 52, 44, 56, 82; but 256 on
-    // 30000, 32 / 8 of 128 MXFP8 624, 223, 161, 174, and 16 of 16 on 4096, MXFP4
-    // 96, 96, 75, 60.
+    // 1531, 12 / 4 heads of 96 MXFP8 36, 25, 27, 32; 4 of 64 on 2048, 32 / 8 of
+    // 128 bf16 46, 33, 31, 38; 128 and 16 on 8192 and 200, 8 / 1 of 64 MXFP4
+    // 22, 20, 24, 31; 3 of 500 on 1000, 8 / 4 of 256 50, 43, 55, 82; 8 of 32 on
+    // 4096, 16 / 2 of 128 50, 29, 32, 40; but 256 on 30000, 32 / 8 of 128 MXFP8
+    // 618, 219, 155, 167, and 16 of 16 on 4096, MXFP4 94, 94, 74, 58.
     int64_t splits = blocks > 0 && blocks < 256 ? 256 / blocks : 1;
     if (splits > units / 2) splits = units / 2;
     p.splits = (int)(splits < 1 ? 1 : splits > 64 ? 64 : splits);

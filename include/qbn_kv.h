@@ -129,8 +129,9 @@ QBN_API int32_t qbn_kv_append(const qbn_kv_cache *cache, int64_t layer, const qb
  * for magnitudes below 2^-116, and for infinities. Products are exact; sums,
  * softmax statistics and accumulators are binary32. The softmax weights are
  * rounded to bfloat16 for the product with V (by 2^-8 of each at most, as much
- * as the output's own rounding), their sum is not. No atomics: repeated calls
- * give bit-identical results.
+ * as the output's own rounding), their sum is not. The sums are divided at the
+ * end: they hold a |v_j| times the number of tokens of 2^100 (of 2^40 where
+ * scores pass 10^7). No atomics: repeated calls give bit-identical results.
  * The work is split over a sequence's length where there are few sequences;
  * the pieces go through `workspace` (device, 16-byte aligned, at least
  * qbn_kv_attention_workspace bytes, not kept: it may be shared by calls that
