@@ -180,7 +180,14 @@ def _need_dtype(t: torch.Tensor, dtypes, name: str):
 
 
 def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """torch's current stream of a device. The default stream's handle is 0 on
+    every device, and a launch on it goes to the current one: refused where
+    that is another."""
+    s = torch.cuda.current_stream(device).cuda_stream
+    if not s and torch.cuda.current_device() != device.index:
+        raise ValueError("the tensors are on %s, which is not the current device: call on its default stream under "
+                         "torch.cuda.device" % device)
+    return ctypes.c_void_p(s)
 
 
 @dataclass
