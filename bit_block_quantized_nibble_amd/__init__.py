@@ -2,7 +2,9 @@
 block-quantized weights (MXFP4, NVFP4, Q4_K), bulk dequantization of six
 formats and bit-exact int4 layout repacks, on AMD MI355X (gfx950). The paged
 key-value cache that a decode step streams next to the weights (append,
-attention, page bookkeeping) is bound in kv.py and exported from here.
+attention, page bookkeeping) is bound in kv.py, the rotation of queries and keys
+by their positions in rotary.py, the mixture-of-experts layer over 4-bit weights
+in experts.py; all are exported from here.
 
 This module only marshals arguments: it checks that every tensor is a
 device tensor holding at least the bytes the call will touch (the C ABI
@@ -26,7 +28,8 @@ __all__ = [
     "QTensor", "QbnError", "RepackRefused", "quantized_gemv", "quantized_gemm", "dequantize", "repack", "validate",
     "validate_async", "nbytes", "status_string", "lib_path", "FORMATS", "Prepared", "prepare_gemv", "prepare_gemm",
     "prepare_dequantize", "prepare_repack", "KVCache", "KVPool", "kv_append", "kv_attention_decode",
-    "kv_attention_prefill", "kv_reserve", "kv_fork", "kv_free", "kv_compact", "kv_nbytes",
+    "kv_attention_prefill", "kv_reserve", "kv_fork", "kv_free", "kv_compact", "kv_nbytes", "Rope", "rope",
+    "rope_frequencies", "kv_append_rope", "MoERouter", "MoE", "moe_route", "moe_experts", "moe", "moe_nbytes",
 ]
 
 FORMATS = {"mxfp4": 1, "nvfp4": 2, "q4_k": 3, "q4_0": 4, "gptq4": 5, "awq4": 6, "nvfp4_cke": 8}
@@ -723,3 +726,5 @@ def prepare_repack(src: QTensor, dst: QTensor, status: torch.Tensor) -> Prepared
 
 from .kv import (KVCache, KVPool, kv_append, kv_attention_decode, kv_attention_prefill, kv_compact,  # noqa: E402
                  kv_fork, kv_free, kv_nbytes, kv_reserve)
+from .experts import MoE, MoERouter, moe, moe_experts, moe_nbytes, moe_route  # noqa: E402
+from .rotary import Rope, kv_append_rope, rope, rope_frequencies  # noqa: E402

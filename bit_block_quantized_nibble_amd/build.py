@@ -3,10 +3,11 @@
 Each .hip source under csrc/ is compiled to an object in _build/ (in
 parallel), then linked into bit_block_quantized_nibble_amd/libqbn.so, next
 to this file, so that the built library travels with the source tree. Next to
-it, _kvcall.so: the Python module that makes the paged cache's calls (host
-code, built with g++ against Python's and torch's headers and linked to
-libqbn.so). Where that one cannot be built, the library is all the same, and
-everything but the paged cache's Python calls runs; the error comes last.
+it, _kvcall.so: the Python module that makes the calls of the paged cache, the
+rotation by positions and the experts' layer (host code, csrc/*.cpp, built with g++
+against Python's and torch's headers and linked to libqbn.so). Where that one
+cannot be built, the library is all the same, and everything but those Python
+calls runs; the error comes last.
 
     python -m bit_block_quantized_nibble_amd.build
 """
@@ -47,22 +48,22 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_calls() -> str:
+def _compile_call(src: str) -> str:
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
-    obj = os.path.join(BUILD, "kv_bind.o")
+    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I" + sysconfig.get_path("include"),
            "-I" + os.path.join(torch, "include"), "-I" + os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-           "-c", os.path.join(CSRC, "kv_bind.cpp"), "-o", obj]
+           "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for kv_bind.cpp:\n%s\n%s" % (r.stdout, r.stderr))
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
     return obj
 
 
-def _link_calls(obj: str) -> None:
+def _link_calls(objs: list) -> None:
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     tmp = CALLS + ".tmp%d" % os.getpid()
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:libqbn.so", "-Wl,-rpath,$ORIGIN",
+    cmd = ["g++", "-shared", "-o", tmp, *objs, "-L" + HERE, "-l:libqbn.so", "-Wl,-rpath,$ORIGIN",
            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -75,7 +76,7 @@ def build(verbose: bool = False) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     jobs = min(len(srcs), max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(jobs) as ex:
-        calls = ex.submit(_compile_calls)
+        calls = [ex.submit(_compile_call, src) for src in sorted(glob.glob(os.path.join(CSRC, "*.cpp")))]
         objs = list(ex.map(_compile, srcs))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-fno-gpu-rdc", "-o", tmp, *objs]
@@ -84,11 +85,12 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
     try:
-        _link_calls(calls.result())
+        _link_calls([c.result() for c in calls])
     except Exception as e:
         if os.path.exists(CALLS):  # of another build: it may not fit this library
             os.remove(CALLS)
-        raise RuntimeError("%s is built, but not %s, which makes the paged cache's Python calls" % (LIB, CALLS)) from e
+        raise RuntimeError("%s is built, but not %s, which makes the Python calls of the paged "
+                           "cache, the rotation and the experts' layer" % (LIB, CALLS)) from e
     if verbose:
         print("built", LIB, CALLS)
     return LIB

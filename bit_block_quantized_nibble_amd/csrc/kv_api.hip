@@ -1,9 +1,11 @@
-// C-ABI entry points of the paged key-value cache: host-side argument checks,
-// then dispatch to the launchers. Nothing is enqueued by a rejected call.
+// C-ABI entry points of the paged key-value cache and of the rotation by
+// positions: host-side argument checks, then dispatch to the launchers. Nothing
+// is enqueued by a rejected call.
 #include <math.h>
 
 #include "kv_launch.h"
 #include "qbn_launch.h"
+#include "rope_launch.h"
 
 namespace {
 
@@ -134,9 +136,99 @@ int32_t check_attention(const qbn_kv_cache *c, int64_t layer, const qbn_kv_batch
     return aligned(out, 16) && aligned(lse, 4) ? QBN_OK : QBN_ERR_ALIGN;
 }
 
+int32_t check_rotation(const qbn_rotation *r, int32_t dim) {
+    if (!r) return QBN_ERR_NULL;
+    if ((r->layout != QBN_ROPE_HALF && r->layout != QBN_ROPE_INTERLEAVED) || r->reserved != 0) return QBN_ERR_FORMAT;
+    if (r->rot <= 0 || r->rot % 16 || r->rot > dim || !isfinite(r->factor)) return QBN_ERR_SHAPE;
+    if (!r->turns) return QBN_ERR_NULL;
+    return aligned(r->turns, 16) ? QBN_OK : QBN_ERR_ALIGN;
+}
+
+// The bytes from the first to the last of [tokens][heads] vectors of `dim` elements.
+uintptr_t extent(int64_t token_stride, int64_t head_stride, int64_t tokens, int64_t heads, int64_t dim, int size) {
+    return ((tokens - 1) * token_stride + (heads - 1) * head_stride + dim) * size;
+}
+bool ranges_apart(const void *a, uintptr_t na, const void *b, uintptr_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x + na <= y || y + nb <= x;
+}
+
+// Vectors to be written: as check_rows, and no two share an element.
+int32_t check_rows_out(const void *p, int64_t token_stride, int64_t head_stride, int64_t tokens, int64_t heads,
+                       int64_t dim, int size) {
+    const int32_t st = check_rows(p, token_stride, head_stride, tokens, heads, size);
+    if (st) return st;
+    const int64_t t = tokens > 1 ? token_stride : INT64_MAX, h = heads > 1 ? head_stride : INT64_MAX;
+    const bool heads_inner = h >= dim && (tokens == 1 || t >= (heads - 1) * head_stride + dim);
+    const bool tokens_inner = t >= dim && (heads == 1 || h >= (tokens - 1) * token_stride + dim);
+    return heads_inner || tokens_inner ? QBN_OK : QBN_ERR_SHAPE;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t qbn_rotation_struct_size(void) { return sizeof(qbn_rotation); }
+
+int32_t qbn_rope(const qbn_rotation *rope, int64_t tokens, int32_t heads, int32_t dim, const int32_t *positions,
+                 const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out, int64_t out_token_stride,
+                 int64_t out_head_stride, int32_t dtype, void *stream) {
+    if (dim <= 0 || dim % 16 || dim > 1024 || tokens < 0 || heads < 0 || heads > (1 << 16) || tokens > kMaxTokens)
+        return QBN_ERR_SHAPE;
+    int32_t st = check_rotation(rope, dim);
+    if (st) return st;
+    if (dtype < QBN_F32 || dtype > QBN_F16) return QBN_ERR_FORMAT;
+    if (dtype == QBN_F16) return QBN_ERR_DTYPE;
+    if (tokens == 0 || heads == 0) return QBN_OK;
+    if (!positions) return QBN_ERR_NULL;
+    if (!aligned(positions, 4)) return QBN_ERR_ALIGN;
+    const int size = dtype == QBN_F32 ? 4 : 2;
+    st = check_rows(x, x_token_stride, x_head_stride, tokens, heads, size);
+    if (!st) st = check_rows_out(out, out_token_stride, out_head_stride, tokens, heads, dim, size);
+    if (st) return st;
+    const bool same = x == out && (tokens == 1 || x_token_stride == out_token_stride) &&
+                      (heads == 1 || x_head_stride == out_head_stride);
+    if (!same && !ranges_apart(x, extent(x_token_stride, x_head_stride, tokens, heads, dim, size), out,
+                               extent(out_token_stride, out_head_stride, tokens, heads, dim, size)))
+        return QBN_ERR_UNSUPPORTED;
+    return hip_status(qbn::launch_rope(*rope, tokens, heads, dim, positions, {x, x_token_stride, x_head_stride},
+                                       {out, out_token_stride, out_head_stride}, dtype, (hipStream_t)stream));
+}
+
+int32_t qbn_kv_append_rope(const qbn_kv_cache *cache, int64_t layer, const qbn_kv_batch *batch,
+                           const qbn_rotation *rope, int32_t q_heads, const void *q, int64_t q_token_stride,
+                           int64_t q_head_stride, void *q_out, int64_t out_token_stride, int64_t out_head_stride,
+                           const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                           int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, void *stream) {
+    int32_t st = check_batch(cache, layer, batch);
+    if (!st) st = check_rotation(rope, cache->head_dim);
+    if (st) return st;
+    if (dtype < QBN_F32 || dtype > QBN_F16) return QBN_ERR_FORMAT;
+    if (dtype == QBN_F16) return QBN_ERR_DTYPE;
+    if (q_heads < 0 || q_heads > (1 << 16)) return QBN_ERR_SHAPE;
+    if (batch->tokens == 0) return QBN_OK;
+    const int64_t tokens = batch->tokens, dim = cache->head_dim;
+    const int size = dtype == QBN_F32 ? 4 : 2;
+    st = check_rows(k, k_token_stride, k_head_stride, tokens, cache->heads, size);
+    if (!st) st = check_rows(v, v_token_stride, v_head_stride, tokens, cache->heads, size);
+    if (!st && q_heads) st = check_rows(q, q_token_stride, q_head_stride, tokens, q_heads, size);
+    if (!st && q_heads) st = check_rows_out(q_out, out_token_stride, out_head_stride, tokens, q_heads, dim, 2);
+    if (st) return st;
+    if (q_heads) {
+        const uintptr_t n = extent(out_token_stride, out_head_stride, tokens, q_heads, dim, 2);
+        const bool same = q == q_out && dtype == QBN_BF16 && (tokens == 1 || q_token_stride == out_token_stride) &&
+                          (q_heads == 1 || q_head_stride == out_head_stride);
+        if (!same &&
+            !(ranges_apart(q, extent(q_token_stride, q_head_stride, tokens, q_heads, dim, size), q_out, n) &&
+              ranges_apart(k, extent(k_token_stride, k_head_stride, tokens, cache->heads, dim, size), q_out, n) &&
+              ranges_apart(v, extent(v_token_stride, v_head_stride, tokens, cache->heads, dim, size), q_out, n)))
+            return QBN_ERR_UNSUPPORTED;
+    }
+    return hip_status(qbn::launch_kv_append_rope(
+        *cache, layer, *batch, *rope, q_heads, {q, q_token_stride, q_head_stride},
+        {q_out, out_token_stride, out_head_stride}, {k, k_token_stride, k_head_stride},
+        {v, v_token_stride, v_head_stride}, dtype, (hipStream_t)stream));
+}
 
 size_t qbn_kv_struct_size(int32_t which) {
     return which == 0 ? sizeof(qbn_kv_cache) : which == 1 ? sizeof(qbn_kv_batch) : which == 2 ? sizeof(qbn_kv_pool) : 0;

@@ -20,8 +20,8 @@
 // 4.95). That is 3 us for the chain of launch, cu, length, table and store, and
 // then the bytes (MXFP4 1.07 us for 1024 tokens, its floor), so that a few
 // thousand tokens take nearly twice their floor.
-#include "kv_device.h"
 #include "kv_launch.h"
+#include "kv_store.h"
 
 namespace qbn {
 namespace {
@@ -51,11 +51,6 @@ __device__ __forceinline__ void floats(const u32x4 (&w)[1], float (&x)[8]) {  //
         x[2 * i] = __uint_as_float(w[0][i] << 16);
         x[2 * i + 1] = __uint_as_float(w[0][i] & 0xFFFF0000u);
     }
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
 
 // A wave takes the same 512 elements of TOK consecutive tokens, whose loads
@@ -120,42 +115,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
             floats(raw[t], x);
             const int64_t head = (int64_t)page[t] * a.heads + h;
             uint8_t *dst = (is_v ? a.v : a.k) + ((head * ps + slot[t]) * a.dim + d) * kBits<F> / 8;
-            if constexpr (F == BF16) {
-                *reinterpret_cast<u32x4 *>(dst) = u32x4{pack2(x[0], x[1]), pack2(x[2], x[3]),
-                                                        pack2(x[4], x[5]), pack2(x[6], x[7])};
-            } else {
-                uint32_t top = 0;  // magnitudes as bit patterns order like the values
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-                top = max(top, dpp_u32<0xB1>(top));  // quad_perm [1,0,3,2]
-                top = max(top, dpp_u32<0x4E>(top));  // quad_perm [2,3,0,1]: the four lanes of the block
-                constexpr int EMAX = F == FP8 ? 8 : 2;
-                int e = (int)(top >> 23) - 127 - EMAX;
-                e = e < -127 ? -127 : (e > 127 ? 127 : e);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_ldexpf(x[i], -e);
-                if constexpr (F == FP8) {
-                    typedef short v2s __attribute__((ext_vector_type(2)));
-                    uint32_t w[2];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = __builtin_fminf(__builtin_fmaxf(x[i], -448.0f), 448.0f);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        v2s p = {0, 0};
-                        p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, x[4 * i], x[4 * i + 1], 1.0f, false);
-                        p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, x[4 * i + 2], x[4 * i + 3], 1.0f, true);
-                        w[i] = __builtin_bit_cast(uint32_t, p);
-                    }
-                    *reinterpret_cast<u32x2 *>(dst) = u32x2{w[0], w[1]};
-                } else {
-                    uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, x[0], x[1], 1.0f, 0);
-                    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], 1.0f, 1);
-                    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], 1.0f, 2);
-                    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], 1.0f, 3);
-                    *reinterpret_cast<uint32_t *>(dst) = w;
-                }
-                exps[t] = e;
-            }
+            exps[t] = put8<F>(dst, x);
         }
         if constexpr (F != BF16) {
             // a lane of the block's four per token: their scales lie side by side

@@ -1,197 +1,17 @@
-// Python entry points of the paged key-value cache's calls (module _kvcall).
+// Python entry points of the paged key-value cache's calls, and the module (_kvcall)
+// of these and the other sources' calls.
 //
 // A decode step's cache calls are kernels of a few microseconds, and a launch
 // takes 2.4 us of host time. Marshalling the arguments through ctypes took 3.4
 // (append) to 5.9 us (attention) beside it, so these calls read the tensors
-// here. Nothing else happens in this file: it checks what the C ABI cannot
+// here. Nothing else happens: it checks what the C ABI cannot
 // see (devices, types, sizes) with the words of kv.py's other checks, allocates
 // what the caller did not give, and returns the C ABI's status.
-#include <Python.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-#include <ATen/ATen.h>
-
-#include <string>
-
-#include "../../include/qbn_kv.h"
+#include "kv_batch.h"
 
 namespace {
 
-struct Refused {};  // a Python error is set
-
-template <typename... A>
-[[noreturn]] void refuse(PyObject *type, const char *form, A... a) {
-    PyErr_Format(type, form, a...);
-    throw Refused{};
-}
-
-std::string words(const at::Tensor &t) { return t.device().str(); }
-
-const at::Tensor &tensor(PyObject *o, const char *name) {
-    if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a tensor", name);
-    return THPVariable_Unpack(o);
-}
-
-void elsewhere(const at::Tensor &t, const char *name) {
-    refuse(PyExc_ValueError, "%s is on %s, the cache or pool on another device", name, words(t).c_str());
-}
-
-int64_t index_of(const at::Tensor &t) { return t.is_cuda() ? t.get_device() : -1; }
-
-void typed(const at::Tensor &t, at::ScalarType want, const char *torch_name, const char *name) {
-    if (t.scalar_type() != want)
-        refuse(PyExc_TypeError, "%s dtype torch.%s (expected %s)", name, c10::toString(t.scalar_type()), torch_name);
-}
-
-// The address of an int32 vector of n entries on device dev.
-int32_t *ints(const at::Tensor &t, int64_t n, int64_t dev, const char *name) {
-    typed(t, at::kInt, "torch.int32", name);
-    if (t.dim() != 1 || !t.is_contiguous()) refuse(PyExc_ValueError, "%s must be a contiguous vector", name);
-    if (t.numel() != n) refuse(PyExc_ValueError, "%s has %lld entries; the call needs %lld", name, (long long)t.numel(), (long long)n);
-    if (index_of(t) != dev) elsewhere(t, name);
-    return (int32_t *)t.data_ptr();
-}
-
-struct Rows {
-    const at::Tensor &t;
-    int64_t token, head;
-};
-
-// Strides of [tokens][heads][dim] vectors (views are taken as they are).
-Rows vectors(const at::Tensor &t, int64_t heads, int64_t dim, int64_t dev, const char *name) {
-    if (t.dim() != 3 || t.size(2) != dim || (heads && t.size(1) != heads))
-        refuse(PyExc_ValueError, "%s must be [tokens][%s][%lld]", name, heads ? std::to_string(heads).c_str() : "heads", (long long)dim);
-    if (t.stride(2) != 1) refuse(PyExc_ValueError, "the last axis of %s must be contiguous", name);
-    if (index_of(t) != dev) elsewhere(t, name);
-    return {t, t.size(0) > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
-}
-
-qbn_kv_batch batch(int64_t dev, int64_t tokens, const at::Tensor &table, const at::Tensor &lens, PyObject *cu) {
-    typed(table, at::kInt, "torch.int32", "table");
-    if (table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1))
-        refuse(PyExc_ValueError, "table must be [seqs][row] with contiguous rows");
-    if (index_of(table) != dev) elsewhere(table, "table");
-    qbn_kv_batch b;
-    b.seqs = table.size(0), b.tokens = tokens, b.row = table.size(1);
-    b.row_stride = b.seqs > 1 ? table.stride(0) : b.row;
-    b.table = (const int32_t *)table.data_ptr();
-    b.cu = nullptr;
-    if (cu == Py_None && tokens != b.seqs)
-        refuse(PyExc_ValueError, "%lld tokens for %lld sequences: one each is wanted without cu", (long long)tokens, (long long)b.seqs);
-    b.lens = ints(lens, b.seqs, dev, "lens");
-    if (cu != Py_None) b.cu = ints(tensor(cu, "cu"), b.seqs + 1, dev, "cu");
-    return b;
-}
-
-// torch's current stream of a device, and the exchange of the current device for
-// another (-1: none) and back, as torch's Python gives them.
-PyObject *g_raw_stream = nullptr, *g_exchange = nullptr, *g_exchange_back = nullptr;
-
-PyObject *with_index(PyObject *f, int64_t dev) {
-    PyObject *arg = PyLong_FromLongLong(dev);
-    PyObject *r = arg ? PyObject_CallOneArg(f, arg) : nullptr;
-    Py_XDECREF(arg);
-    return r;
-}
-
-// A call's stream, with its device as the current one while this lives: the
-// default stream's handle is 0 on every device, and a launch on it goes to the
-// current one.
-class OnDevice {
-  public:
-    explicit OnDevice(int64_t dev) {
-        PyObject *r = with_index(g_exchange, dev);
-        if (!r) throw Refused{};
-        before_ = PyLong_AsLongLong(r);
-        Py_DECREF(r);
-        moved_ = before_ >= 0 && before_ != dev;
-        r = with_index(g_raw_stream, dev);
-        if (r) {
-            stream_ = PyLong_AsVoidPtr(r);
-            Py_DECREF(r);
-        }
-        if (!stream_ && PyErr_Occurred()) {
-            back();
-            throw Refused{};
-        }
-    }
-    OnDevice(const OnDevice &) = delete;
-    ~OnDevice() { back(); }
-    operator void *() const { return stream_; }
-
-  private:
-    void back() {
-        if (!moved_) return;
-        moved_ = false;
-        PyObject *type, *value, *trace;  // an error on its way is kept
-        PyErr_Fetch(&type, &value, &trace);
-        PyObject *r = with_index(g_exchange_back, before_);
-        if (r) Py_DECREF(r);
-        else PyErr_WriteUnraisable(g_exchange_back);
-        PyErr_Restore(type, value, trace);
-    }
-    int64_t before_ = -1;
-    bool moved_ = false;
-    void *stream_ = nullptr;
-};
-
-int64_t integer(PyObject *o) {
-    const long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) throw Refused{};
-    return v;
-}
-// The C ABI refuses what does not fit its 32-bit arguments' ranges; the value must not wrap into them first.
-int32_t int32(PyObject *o) {
-    const int64_t v = integer(o);
-    return v > INT32_MAX || v < INT32_MIN ? INT32_MIN : (int32_t)v;
-}
-
-// A handle: the bytes of its C struct, made by kv.py.
-template <typename T>
-const T *handle(PyObject *o) {
-    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != sizeof(T)) refuse(PyExc_TypeError, "not a handle of this library");
-    return reinterpret_cast<const T *>(PyBytes_AS_STRING(o));
-}
-
-// The workspace of a call: the caller's, or one of `need` bytes.
-struct Workspace {
-    at::Tensor keep;
-    void *p = nullptr;
-    int64_t bytes = 0;
-};
-Workspace workspace(PyObject *given, int64_t need, int64_t dev, const at::Tensor &like) {
-    Workspace w;
-    if (given != Py_None) {
-        const at::Tensor &t = tensor(given, "workspace");
-        const int64_t have = t.numel() * t.element_size();
-        if (have < need)
-            refuse(PyExc_ValueError, "workspace holds %lld bytes; the call needs %lld", (long long)have, (long long)need);
-        if (!t.is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
-        if (index_of(t) != dev) elsewhere(t, "workspace");
-        w.p = t.data_ptr(), w.bytes = have;
-    } else if (need > 0) {
-        w.keep = at::empty({need}, like.options().dtype(at::kByte));
-        w.p = w.keep.data_ptr(), w.bytes = need;
-    }
-    return w;
-}
-
-template <typename F>
-PyObject *guarded(F f) {
-    try {
-        return f();
-    } catch (const Refused &) {
-    } catch (...) {  // torch's, the allocator's torch.OutOfMemoryError above all: as torch's own functions raise it
-        torch::translate_exception_to_python(std::current_exception());
-    }
-    return nullptr;
-}
-
-bool count_is(Py_ssize_t n, Py_ssize_t want) {
-    if (n == want) return true;
-    PyErr_Format(PyExc_TypeError, "%zd arguments, %zd wanted", n, want);
-    return false;
-}
+using namespace qcall;
 
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {  // cache, device, k, v, table, lens, cu, layer
     if (!count_is(n, 8)) return nullptr;
@@ -360,11 +180,13 @@ PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {  // cache, in,
 }
 
 #define QBN_METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {QBN_METHOD(append), QBN_METHOD(attention), QBN_METHOD(pool),    QBN_METHOD(pool_like), QBN_METHOD(reserve),
-                           QBN_METHOD(fork),   QBN_METHOD(release),   QBN_METHOD(compact), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {QBN_METHOD(append),    QBN_METHOD(attention),   QBN_METHOD(pool),    QBN_METHOD(pool_like),
+                           QBN_METHOD(reserve),   QBN_METHOD(fork),        QBN_METHOD(release), QBN_METHOD(compact),
+                           QBN_METHOD(rope),      QBN_METHOD(append_rope), QBN_METHOD(moe_route),
+                           QBN_METHOD(moe_experts), QBN_METHOD(moe),       {nullptr, nullptr, 0, nullptr}};
 #undef QBN_METHOD
 
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_kvcall", "Calls of the paged key-value cache.", -1, g_methods,
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_kvcall", "Calls of the paged key-value cache, the rotation by positions and the experts' layer.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

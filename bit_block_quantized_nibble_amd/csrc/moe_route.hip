@@ -1,0 +1,217 @@
+// Choosing the experts of each token: logits, the top_k of them, their weights.
+//
+// Which expert comes next may hang on the last bit of a logit, so the sums are
+// binary64: products of bfloat16 values are exact, and the order of a sum of
+// thousands of them then moves it by 1e-16 instead of 1e-7. The vector units do a
+// binary64 fma at the rate of a binary32 one, and the matrix cores do as many.
+//
+// Few tokens: a workgroup per expert, its row read once and multiplied with each
+// token's; bound by latency. More: 16 tokens by 16 experts a workgroup on the
+// matrix cores, k split over its waves; bound by binary64 products from about 100
+// tokens on. Then a wave per token finds the best one after the other.
+#include "kv_device.h"
+#include "moe_launch.h"
+#include "rope_device.h"
+
+namespace qbn {
+namespace {
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+constexpr int64_t kPortion = 4096;  // tokens whose logits the workspace holds at a time
+constexpr int kFew = 4;             // tokens of the vector form
+
+struct Args {
+    const __bf16 *x, *w;
+    const float *bias;
+    double *logits;  // [tokens][experts]
+    int32_t *ids;
+    float *weights;
+    int64_t xs;
+    int tokens, experts, hidden, top, normalize;
+};
+
+// The sum over a wave's lanes, in all of them.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+
+template <int T>
+__global__ __launch_bounds__(256) void k_logits_few(Args a) {
+    __shared__ double part[4][T];
+    const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double sum[T] = {};
+    for (int k = threadIdx.x * 8; k < a.hidden; k += 256 * 8) {
+        float w[8], x[8];
+        rope::floats(rope::load8(a.w + (int64_t)e * a.hidden + k), w);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            rope::floats(rope::load8(a.x + min(t, a.tokens - 1) * a.xs + k), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[t] = __builtin_fma((double)w[i], (double)x[i], sum[t]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const double s = wave_sum(sum[t]);
+        if (lane == 0) part[wave][t] = s;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < T && (int)threadIdx.x < a.tokens) {
+        double s = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+        if (a.bias) s += (double)a.bias[e];
+        a.logits[(int64_t)threadIdx.x * a.experts + e] = s;
+    }
+}
+
+// 16 tokens x 16 experts. A wave's k come in pieces of 32, of which the lanes of a
+// quarter (16 lanes) have eight in a row each: which k a product step takes is
+// free, as long as both operands agree.
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void k_logits(Args a) {
+    __shared__ double part[WAVES][256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quarter = lane >> 4;
+    const int tiles = (a.experts + 15) / 16;
+    const int t0 = (int)(blockIdx.x / tiles) * 16, e0 = (int)(blockIdx.x % tiles) * 16;
+    const __bf16 *x = a.x + (int64_t)min(t0 + row, a.tokens - 1) * a.xs + quarter * 8;
+    const __bf16 *w = a.w + (int64_t)min(e0 + row, a.experts - 1) * a.hidden + quarter * 8;
+    f64x4 acc = {0, 0, 0, 0};
+    for (int k = wave * 32; k < a.hidden; k += WAVES * 32) {
+        float u[8], v[8];
+        rope::floats(rope::load8(x + k), u);
+        rope::floats(rope::load8(w + k), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)u[i], (double)v[i], acc, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[wave][(quarter + 4 * i) * 16 + row] = acc[i];  // token quarter + 4 i, expert row
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += WAVES * 64) {
+        double s = 0.0;
+#pragma unroll
+        for (int j = 0; j < WAVES; ++j) s += part[j][i];
+        const int t = t0 + i / 16, e = e0 + i % 16;
+        if (t < a.tokens && e < a.experts) {
+            if (a.bias) s += (double)a.bias[e];
+            a.logits[(int64_t)t * a.experts + e] = s;
+        }
+    }
+}
+
+// Numbers as unsigned words of the same order, all of them above 0; NaN as -inf.
+__device__ __forceinline__ uint64_t ordered(double v) {
+    if (v != v) v = -__builtin_huge_val();
+    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 is 0
+    return b ^ (b >> 63 ? ~(uint64_t)0 : (uint64_t)1 << 63);
+}
+__device__ __forceinline__ double number(uint64_t b) {
+    return __builtin_bit_cast(double, b ^ (b >> 63 ? (uint64_t)1 << 63 : ~(uint64_t)0));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t max_dpp(uint64_t v) {
+    const uint64_t o = (uint64_t)(uint32_t)kv::dpp_i32<CTRL, ROWS>((int)(uint32_t)v) |
+                       (uint64_t)(uint32_t)kv::dpp_i32<CTRL, ROWS>((int)(uint32_t)(v >> 32)) << 32;
+    return o > v ? o : v;
+}
+// The largest over a wave's lanes, the same in all of them.
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    v = max_dpp<0x111, 0xF>(v);  // shifts within rows of 16, then rows into the next (lanes without a source read 0)
+    v = max_dpp<0x112, 0xF>(v);
+    v = max_dpp<0x114, 0xF>(v);
+    v = max_dpp<0x118, 0xF>(v);
+    v = max_dpp<0x142, 0xA>(v);
+    v = max_dpp<0x143, 0xC>(v);
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63) |
+           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63) << 32;
+}
+
+// A wave per token; lane l has experts l, l + 64, ... (EACH of them).
+template <int EACH>
+__global__ __launch_bounds__(256) void k_choose(Args a) {
+    const int lane = threadIdx.x & 63;
+    const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (t >= a.tokens) return;
+    uint64_t key[EACH];
+    double total = 0.0;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+        const int e = lane + 64 * j;
+        const double v = e < a.experts ? a.logits[(int64_t)t * a.experts + e] : 0.0;
+        key[j] = e < a.experts ? ordered(v) : 0;
+        nan = nan || v != v;
+    }
+    nan = __ballot(nan) != 0;
+    uint64_t first = key[0];
+#pragma unroll
+    for (int j = 1; j < EACH; ++j) first = key[j] > first ? key[j] : first;
+    first = wave_max(first);
+    const double best = number(first);
+    if (!a.normalize) {
+        double s = 0.0;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j)
+            if (key[j]) s += exp(number(key[j]) - best);
+        total = wave_sum(s);
+    }
+    int id = 0;         // lane j: the j-th expert
+    double mine = 0.0;  // and its logit
+    for (int r = 0; r < a.top; ++r) {
+        uint64_t top = key[0];
+#pragma unroll
+        for (int j = 1; j < EACH; ++j) top = key[j] > top ? key[j] : top;
+        top = wave_max(top);
+        int e = 0x7FFFFFFF;
+#pragma unroll
+        for (int j = EACH - 1; j >= 0; --j) {  // the lowest number among equal ones
+            const uint64_t m = __ballot(key[j] == top);
+            if (m) e = 64 * j + __builtin_ctzll(m);
+        }
+#pragma unroll
+        for (int j = 0; j < EACH; ++j)
+            if (e == lane + 64 * j) key[j] = 0;
+        if (lane == r) id = e, mine = number(top);
+    }
+    double p = lane < a.top ? exp(mine - best) : 0.0;
+    if (a.normalize) total = wave_sum(p);
+    if (nan) total = __builtin_nan("");
+    if (lane < a.top) {
+        a.ids[(int64_t)t * a.top + lane] = id;
+        a.weights[(int64_t)t * a.top + lane] = (float)(p / total);
+    }
+}
+
+}  // namespace
+
+int64_t moe_route_workspace(const qbn_moe_router &r, int64_t tokens) {
+    return 8 * (tokens < kPortion ? tokens : kPortion) * r.experts;
+}
+
+hipError_t launch_moe_route(const qbn_moe_router &r, int64_t tokens, const void *x, int64_t x_stride, int32_t *ids,
+                            float *weights, void *ws, hipStream_t s) {
+    for (int64_t at = 0; at < tokens; at += kPortion) {
+        Args a;
+        a.x = (const __bf16 *)x + at * x_stride, a.w = (const __bf16 *)r.weight, a.bias = r.bias;
+        a.logits = (double *)ws, a.ids = ids + at * r.top_k, a.weights = weights + at * r.top_k;
+        a.xs = x_stride, a.tokens = (int)(tokens - at < kPortion ? tokens - at : kPortion);
+        a.experts = r.experts, a.hidden = r.hidden, a.top = r.top_k, a.normalize = r.normalize;
+        if (a.tokens <= kFew) {
+            (a.tokens == 1 ? k_logits_few<1> : a.tokens == 2 ? k_logits_few<2> : k_logits_few<4>)<<<r.experts, 256, 0, s>>>(a);
+        } else {
+            const int tiles = (a.tokens + 15) / 16 * ((r.experts + 15) / 16);
+            if (tiles < 256) k_logits<16><<<tiles, 1024, 0, s>>>(a);
+            else k_logits<8><<<tiles, 512, 0, s>>>(a);
+        }
+        const int blocks = (a.tokens + 3) / 4, each = (r.experts + 63) / 64;
+        (each <= 1 ? k_choose<1> : each <= 2 ? k_choose<2> : each <= 4 ? k_choose<4> : each <= 8 ? k_choose<8> : k_choose<16>)
+            <<<blocks, 256, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace qbn
