@@ -1,4 +1,4 @@
-// The experts' layer over 4-bit weights, for a few tokens.
+// The experts' layer over 4-bit weights.
 //
 //   out_t = sum_j w_tj W2[e] (silu(Wg[e] x_t) * (Wu[e] x_t)),  e = ids[t][j]
 // An assignment a = t * top_k + j is a token's j-th expert. Bound by the weights'
@@ -12,15 +12,12 @@
 // product steps: which k a step takes is free as long as the columns agree, and
 // they have the same 8 elements each in one 16-byte load of x.
 //
-// First kernel: h for each assignment, 16 gate rows and the 16 up rows beside them
-// per workgroup, k split over its four waves and joined in LDS. h goes on as two
-// bfloat16 values, the upper bits and the rest: one alone would round it by 2^-9,
-// as much as the output's own rounding. Second kernel: the same products with W2.
-// Where assignments are few (64), a workgroup has 16 output rows of all of them and
-// adds up the tokens' experts itself; else the assignments' results go to memory
-// and a third kernel adds them.
-#include <type_traits>
-
+// First kernel: h for each assignment, from 16 gate rows and the 16 up rows beside them.
+// h goes on as two bfloat16 values, the upper bits and the rest: one alone would round it
+// by 2^-9, as much as the output's own rounding. Second kernel: the same products with
+// W2. Where tokens are few, a workgroup has 16 output rows of all of them and adds up the
+// tokens' experts itself; else the assignments' results go to memory and one more kernel
+// adds them, in the order of a token's choices: the same bits every time.
 #include "kv_device.h"
 #include "moe_launch.h"
 
@@ -41,90 +38,43 @@ struct Args {
     int64_t xs, os;
     uint16_t *hi, *lo;  // h [assignments][inter], upper bits and rest
     float *y;           // [assignments][hidden]: results of W2, weighted (many assignments)
-    const int32_t *list, *start, *active;  // many: assignments by expert, where each expert's start, the experts that have any
+    const int32_t *list;  // more tokens: assignments by expert
+    const int4 *slots;    // and each expert that has any: {its number, where its list begins, how many}; then {-1}
     int tokens, top, n, experts, hidden, inter;  // n: assignments
 };
 
-// A weight row's 32 elements and their scales.
-struct Piece {
-    u32x4 codes;
-    uint32_t scale;
+// 16 weight rows of k elements: where they start, the same in the whole wave. A lane's
+// row (lane % 16) and block lie less than 2^32 bytes beyond.
+struct Tile {
+    const uint8_t *w, *s;
 };
 template <int F>
-__device__ __forceinline__ Piece load_piece(const uint8_t *w, const uint8_t *s, int block) {
-    Piece p;
-    p.codes = ld16(w + (int64_t)block * 16);
-    if constexpr (F == MX) p.scale = s[block];
-    else p.scale = *reinterpret_cast<const uint16_t *>(s + 2 * block);
-    return p;
+__device__ __forceinline__ Tile tile_of(const uint8_t *w, const uint8_t *s, int64_t row, int k) {
+    return {w + row * (k / 2), s + row * (k / (F == MX ? 32 : 16))};
 }
-// Word i of a piece: eight elements as bfloat16, exact.
 template <int F>
-__device__ __forceinline__ bf16x8 expand(const Piece &p, int i) {
-    const uint32_t c = p.codes[i];
+__device__ __forceinline__ const uint8_t *scales_end(const uint8_t *s, const Args &a, int rows, int k) {
+    return s + (int64_t)a.experts * rows * (k / (F == MX ? 32 : 16));
+}
+
+// Eight elements, word i of a row's 32, as bfloat16, exact. scale: the 32's byte, or
+// both bytes of NVFP4.
+template <int F>
+__device__ __forceinline__ bf16x8 expand(uint32_t c, uint32_t scale, int i) {
     u32x4 o;
     if constexpr (F == MX) {
-        const float s = kv::e8m0_operand(p.scale);
+        const float s = kv::e8m0_operand(scale);
         o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
         o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
         o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
         o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
     } else {
-        const float s = e4m3fn_f32(i < 2 ? p.scale & 0xFFu : p.scale >> 8);
+        const float s = e4m3fn_f32(i < 2 ? scale & 0xFFu : scale >> 8);
         const f32x2 a = e2m1x2_f32<0>(c), b = e2m1x2_f32<1>(c), d = e2m1x2_f32<2>(c), e = e2m1x2_f32<3>(c);
         o = u32x4{kv::pack2(a.x * s, a.y * s), kv::pack2(b.x * s, b.y * s), kv::pack2(d.x * s, d.y * s),
                   kv::pack2(e.x * s, e.y * s)};
     }
     return kv::as_bf16x8(o);
-}
-
-// acc[i][m] += rows i of 16 weights x columns of 16 vectors m, over the steps (of 128
-// elements) from `first` on, `every` apart. w, s: this lane's row (lane % 16) of each
-// tile; x, xl: its column (lane % 16) of each, upper bits and rest.
-template <int F, int NT, int MT, bool LO>
-__device__ __forceinline__ void products(const uint8_t *const (&w)[NT], const uint8_t *const (&s)[NT],
-                                         const uint16_t *const (&x)[MT], const uint16_t *const (&xl)[MT], int k,
-                                         int first, int every, f32x4 (&acc)[NT][MT]) {
-    const int quarter = (threadIdx.x & 63) >> 4, blocks = k / 32, steps = (blocks + 3) / 4;
-    const auto step = [&](int t, auto tail) {
-        int block = 4 * t + quarter;
-        const bool in = !tail || block < blocks;
-        if (tail && !in) block = blocks - 1;
-        Piece p[NT];
-        bf16x8 v[MT][4], l[MT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) p[i] = load_piece<F>(w[i], s[i], block);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[m][j] = kv::as_bf16x8(ld16(x[m] + block * 32 + 8 * j));
-                if (LO) l[m][j] = kv::as_bf16x8(ld16(xl[m] + block * 32 + 8 * j));
-            }
-        if (tail && !in) {  // beyond the row: nothing, whatever its last block has
-#pragma unroll
-            for (int i = 0; i < NT; ++i) p[i] = {u32x4{0, 0, 0, 0}, 0};
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[m][j] = l[m][j] = kv::as_bf16x8(u32x4{0, 0, 0, 0});
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const bf16x8 a = expand<F>(p[i], j);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, v[m][j], acc[i][m], 0, 0, 0);
-                    if (LO) acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, l[m][j], acc[i][m], 0, 0, 0);
-                }
-            }
-    };
-    const int whole = blocks / 4;
-    int t = first;
-    for (; t < whole; t += every) step(t, std::false_type{});
-    if (t < steps) step(t, std::true_type{});
 }
 
 // The upper bits of h, and what they leave out, both bfloat16. Cut, not rounded: the
@@ -151,144 +101,547 @@ __device__ __forceinline__ uint64_t same_expert(int id, bool valid, int slot, in
     const uint64_t m = __ballot(valid && id == expert);
     return m && __builtin_ctzll(m) == slot ? m : 0;
 }
-
-// The workgroup's expert and its assignments (in LDS or memory). False: nothing to do.
-template <bool FEW>
-__device__ __forceinline__ bool find(const Args &a, int slot, int *lds, int &expert, int &n, const int *&list) {
-    if constexpr (FEW) {
-        const int lane = threadIdx.x & 63, id = lane < a.n ? a.ids[lane] : -1;
-        const bool valid = (uint32_t)id < (uint32_t)a.experts;
-        const uint64_t m = same_expert(id, valid, slot, expert);
-        n = __popcll(m);
-        if (!m) return false;
-        if (threadIdx.x < 64 && (m >> lane & 1)) lds[__popcll(m & (((uint64_t)1 << lane) - 1))] = lane;
-        list = lds;
-        __syncthreads();
-    } else {
-        expert = a.active[slot];
-        if (expert < 0) return false;
-        const int at = a.start[expert];
-        n = a.start[expert + 1] - at;
-        list = a.list + at;
-    }
-    return true;
+// The lane of the i-th bit of m.
+__device__ __forceinline__ int nth_bit(uint64_t m, int i) {
+    for (; i > 0; --i) m &= m - 1;
+    return __builtin_ctzll(m);
 }
 
-constexpr int kWaves = 4;
+// Loads go out here, in this order, not where they are used.
+__device__ __forceinline__ void fix() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
 
-// Sums of the waves' accumulators, through LDS: value (row, column) of tile (i, m).
-template <int NT, int MT>
-struct Joined {
-    float v[kWaves][NT * MT][256];
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// ---------------------------------------------------------------- scales
+//
+// A step of 256 elements wants 8 bytes of each row's scales (16 with NVFP4), from as many
+// lines as the codes' 128: read with each step, they cost a third of the rate. So those of
+// kSpan elements of 32 rows are copied into LDS first, 16 bytes a lane.
+constexpr int kScaleBytes = 128;                 // of a row, that LDS holds
+constexpr int kScalePitch = kScaleBytes + 16;    // so that 16 rows lie in as many banks
+template <int F>
+constexpr int kSpan = kScaleBytes * (F == MX ? 32 : 16);  // and their elements
+
+// 16 bytes from s on, at any alignment; those from `end` on read as 0, and no byte there is touched
+// (16 bytes lie before it).
+__device__ __forceinline__ u32x4 ld16_before(const uint8_t *s, const uint8_t *end) {
+    const uint32_t beyond = s > end - 16 ? (uint32_t)(s - (end - 16)) : 0;
+    u32x4 v;
+    __builtin_memcpy(&v, s - beyond, 16);
+    if (beyond & 8) v = u32x4{v.z, v.w, 0, 0};
+    if (beyond & 4) v = u32x4{v.y, v.z, v.w, 0};
+    return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, beyond), __builtin_amdgcn_alignbyte(v.z, v.y, beyond),
+                 __builtin_amdgcn_alignbyte(v.w, v.z, beyond), __builtin_amdgcn_alignbyte(0, v.w, beyond)};
+}
+
+// `count` blocks' scales, from block `first` on, of two tiles into LDS, by each wave (WAVES 1) or by four
+// together. end: of all scales. then(): called when the loads are on their way and before they are waited for.
+template <int F, int WAVES, typename Then>
+__device__ __forceinline__ void copy_scales(uint8_t *lds, const Tile (&tiles)[2], const uint8_t *end, uint32_t blocks,
+                                            uint32_t first, uint32_t count, const Then &then) {
+    constexpr int EACH = F == MX ? 1 : 2, LOADS = 4 / WAVES;  // bytes of a block
+    const uint32_t i = threadIdx.x & (64 * WAVES - 1);
+    u32x4 v[LOADS];
+#pragma unroll
+    for (int l = 0; l < LOADS; ++l) {
+        const uint32_t row = (i + l * 64) / 8, at = i % 8 * 16;
+        v[l] = ld16_before((row < 16 ? tiles[0].s : tiles[1].s) + (((row & 15) * blocks + first) * EACH + (at < count * EACH ? at : 0)), end);
+    }
+    fix();
+    then();
+#pragma unroll
+    for (int l = 0; l < LOADS; ++l)
+        *reinterpret_cast<u32x4 *>(lds + (i + l * 64) / 8 * kScalePitch + i % 8 * 16) = v[l];
+}
+// The scale, or both, of a block: row of 32, block of those that LDS has.
+template <int F>
+__device__ __forceinline__ uint32_t scale_of(const uint8_t *lds, int row, uint32_t block) {
+    const uint8_t *s = lds + row * kScalePitch + block * (F == MX ? 1 : 2);
+    if constexpr (F == MX) return *s;
+    else return *reinterpret_cast<const uint16_t *>(s);
+}
+
+// ---------------------------------------------------------------- few tokens
+//
+// Each wave has its own part of k, all of whose loads it sends at once, and x (or h)
+// lies in LDS as a whole: rows of `pitch` bytes, padded with zeros to whole pairs of steps.
+// A step is 128 elements, 32 for each quarter of the lanes.
+constexpr int kFewTokens = 8;
+
+__host__ __device__ constexpr int few_pitch(int k) { return (k + 255) / 256 * 512 + 16; }
+
+// Vectors of k bfloat16 values into LDS by a workgroup of WAVES waves, each 64 parts of 16 bytes of one
+// vector at a time, AHEAD of those at once. from(r): where vector r lies. then(): as above.
+template <int WAVES, int AHEAD, typename From, typename Then>
+__device__ __forceinline__ void stage(uint8_t *lds, int rows, int k, const From &from, const Then &then) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t each = (k + 255) / 256 * 32, turns = (each + 63) / 64, total = rows * turns;
+    const uint32_t inverse = turns > 1 ? 0xFFFFFFFFu / turns + 1 : 0;  // i / turns: i < 2^13
+    const int pitch = few_pitch(k);
+    const auto row_of = [&](uint32_t i) { return turns > 1 ? __umulhi(i, inverse) : i; };
+    for (uint32_t i0 = wave;; i0 += WAVES * AHEAD) {
+        u32x4 v[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const uint32_t i = min(i0 + u * WAVES, total - 1), r = row_of(i), at = (i - r * turns) * 64 + lane;
+            const bool in = (int)at * 8 < k;
+            v[u] = ld16(from((int)r) + (in ? at * 8 : 0));
+            if (!in) v[u] = u32x4{0, 0, 0, 0};
+        }
+        if (i0 == (uint32_t)wave) {
+            fix();
+            then();
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const uint32_t i = i0 + u * WAVES, r = row_of(i), at = (i - r * turns) * 64 + lane;
+            if (i < total && at < each) *reinterpret_cast<u32x4 *>(lds + r * pitch + at * 16) = v[u];
+        }
+        if (i0 + WAVES * AHEAD >= total) break;
+    }
+}
+
+// COUNT pairs of steps from `first`, `every` apart, of NT tiles. In pairs, since a
+// row's two 64-byte halves of a line go through the first cache together then.
+template <int F, int NT, int COUNT>
+struct Batch {
+    u32x4 codes[COUNT][2][NT];
+    uint32_t scale[COUNT][2][NT];
+
+    __device__ __forceinline__ void load(const Tile (&tiles)[NT], uint32_t blocks, uint32_t first, uint32_t every) {
+        const uint32_t lane = threadIdx.x & 63, row = (lane & 15) * blocks;
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // beyond the row: its last block, and x is 0 there or not looked at
+                    const uint32_t at = row + min(8 * (first + u * every) + 4 * h + (lane >> 4), blocks - 1);
+                    codes[u][h][i] = ld16(tiles[i].w + at * 16);
+                    if constexpr (F == MX) scale[u][h][i] = tiles[i].s[at];
+                    else scale[u][h][i] = *reinterpret_cast<const uint16_t *>(tiles[i].s + 2 * at);
+                }
+    }
+    // Pairs below `pairs`. x: this lane's column in LDS, at its quarter
+    __device__ __forceinline__ void multiply(const uint8_t *x, int pairs, int first, int every, f32x4 (&acc)[NT]) const {
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) {
+            const int d = first + u * every;
+            if (COUNT > 1 && d >= pairs) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bf16x8 v = kv::as_bf16x8(ld16(x + d * 512 + h * 256 + 16 * j));
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand<F>(codes[u][h][i][j], scale[u][h][i], j), v,
+                                                                         acc[i], 0, 0, 0);
+                }
+        }
+    }
 };
 
-template <int F, int MT>
-__device__ __forceinline__ void gate_up(const Args &a, float *lds, int tile, int expert, int n, const int *list) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quarter = lane >> 4;
-    const uint8_t *w[2], *s[2];
-    constexpr int SB = F == MX ? 32 : 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t r = (int64_t)expert * 2 * a.inter + i * a.inter + tile * 16 + row;
-        w[i] = a.w13 + r * (a.hidden / 2);
-        s[i] = a.s13 + r * (a.hidden / SB);
-    }
-    const uint16_t *x[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = a.x + (int64_t)(list[min(16 * m + row, n - 1)] / a.top) * a.xs;
-    f32x4 acc[2][MT] = {};
-    products<F, 2, MT, false>(w, s, x, x, a.hidden, wave, kWaves, acc);
-    auto *joined = reinterpret_cast<Joined<2, MT> *>(lds);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)  // rows 4 quarter .. + 3 of column `row`
-            *reinterpret_cast<f32x4 *>(&joined->v[wave][i * MT + m][row * 16 + quarter * 4]) = acc[i][m];
-    __syncthreads();
-    const float f = F == NV ? a.f13[expert] : 1.0f;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int c = 16 * m + threadIdx.x / 16;
-        if (c >= n) continue;
-        float g = 0.0f, u = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kWaves; ++j) {
-            g += joined->v[j][m][threadIdx.x];
-            u += joined->v[j][MT + m][threadIdx.x];
-        }
-        const int64_t to = (int64_t)list[c] * a.inter + tile * 16 + threadIdx.x % 16;
-        split(silu(g * f) * (u * f), a.hi[to], a.lo[to]);
-    }
-    __syncthreads();
-}
+// A workgroup has 16 gate and 16 up rows; its four waves split the pairs of steps among them and join
+// their sums in LDS. What LDS has to have before the first product is loaded first, and the codes
+// right after it, all of a span's: they then arrive while the first are multiplied.
+constexpr int kGateWaves = 4;
 
-template <int F, bool FEW>
-__global__ __launch_bounds__(256) void k_gate_up(Args a) {
-    __shared__ __attribute__((aligned(16))) float lds[sizeof(Joined<2, 4>) / 4];
-    __shared__ int list_lds[64];
-    int expert, n;
-    const int *list;
-    if (!find<FEW>(a, blockIdx.y, list_lds, expert, n, list)) return;
-    for (; n > 0; n -= 64, list += 64) {
-        if (n <= 16) gate_up<F, 1>(a, lds, blockIdx.x, expert, n, list);
-        else if (n <= 32) gate_up<F, 2>(a, lds, blockIdx.x, expert, n, list);
-        else gate_up<F, 4>(a, lds, blockIdx.x, expert, min(n, 64), list);
-    }
-}
-
-template <int F, int MT>
-__device__ __forceinline__ void down(const Args &a, float *lds, int tile, int expert, int n, const int *list) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quarter = lane >> 4;
-    const uint8_t *w[2], *s[2];
-    constexpr int SB = F == MX ? 32 : 16;
+// acc += a wave's part of a span, TURNS pairs of steps or fewer. x: this lane's column in LDS, at its quarter
+template <int F, int TURNS, typename Stage>
+__device__ __forceinline__ void gate_up_span(uint8_t *scales, const Tile (&tiles)[2], const uint8_t *end, uint32_t blocks, uint32_t start,
+                                             uint32_t here, const uint8_t *x, const Stage &stage_x, f32x4 (&acc)[2]) {
+    const uint32_t lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pairs = (here + 7) / 8;
+    u32x4 p[TURNS][2][2];
+    copy_scales<F, kGateWaves>(scales, tiles, end, blocks, start, here, [&] {
+        stage_x([&] {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t r = (int64_t)expert * a.hidden + tile * 32 + i * 16 + row;
-        w[i] = a.w2 + r * (a.inter / 2);
-        s[i] = a.s2 + r * (a.inter / SB);
-    }
-    const uint16_t *x[MT], *xl[MT];
+            for (int u = 0; u < TURNS; ++u)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t at = (int64_t)list[min(16 * m + row, n - 1)] * a.inter;
-        x[m] = a.hi + at, xl[m] = a.lo + at;
-    }
-    f32x4 acc[2][MT] = {};
-    products<F, 2, MT, true>(w, s, x, xl, a.inter, wave, kWaves, acc);
-    auto *joined = reinterpret_cast<Joined<2, MT> *>(lds);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+                    for (int h = 0; h < 2; ++h)
+                        p[u][h][i] = ld16(tiles[i].w + (row * blocks + start +
+                                                        min(8 * (wave + u * kGateWaves) + 4 * h + quarter, here - 1)) * 16);
+            fix();
+        });
+    });
+    lds_barrier();
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            *reinterpret_cast<f32x4 *>(&joined->v[wave][i * MT + m][row * 16 + quarter * 4]) = acc[i][m];
-    __syncthreads();
-    const float f = F == NV ? a.f2[expert] : 1.0f;
+    for (int u = 0; u < TURNS; ++u) {
+        const int d = wave + u * kGateWaves;
+        if (d >= pairs) break;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int c = 16 * m + threadIdx.x / 16;
-        if (c >= n) continue;
-        const float weight = a.weights[list[c]] * f;
+        for (int h = 0; h < 2; ++h) {
+            uint32_t scale[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float v = 0.0f;
+            for (int i = 0; i < 2; ++i) scale[i] = scale_of<F>(scales, i * 16 + row, min(8 * d + 4 * h + quarter, here - 1));
 #pragma unroll
-            for (int j = 0; j < kWaves; ++j) v += joined->v[j][i * MT + m][threadIdx.x];
-            a.y[(int64_t)list[c] * a.hidden + tile * 32 + i * 16 + threadIdx.x % 16] = v * weight;
+            for (int j = 0; j < 4; ++j) {
+                const bf16x8 v = kv::as_bf16x8(ld16(x + d * 512 + h * 256 + 16 * j));
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand<F>(p[u][h][i][j], scale[i], j), v, acc[i], 0, 0, 0);
+            }
         }
     }
-    __syncthreads();
 }
 
 template <int F>
-__global__ __launch_bounds__(256) void k_down(Args a) {
-    __shared__ __attribute__((aligned(16))) float lds[sizeof(Joined<2, 4>) / 4];
-    int expert, n;
-    const int *list;
-    if (!find<false>(a, blockIdx.y, nullptr, expert, n, list)) return;
-    for (; n > 0; n -= 64, list += 64) {
-        if (n <= 16) down<F, 1>(a, lds, blockIdx.x, expert, n, list);
-        else if (n <= 32) down<F, 2>(a, lds, blockIdx.x, expert, n, list);
-        else down<F, 4>(a, lds, blockIdx.x, expert, min(n, 64), list);
+__global__ __launch_bounds__(kGateWaves * 64, 3) void k_gate_up_few(Args a, int slots) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t xs[];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[32 * kScalePitch];
+    __shared__ __attribute__((aligned(16))) float joined[kGateWaves][2][kFewTokens][16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15;
+    const uint32_t quarter = lane >> 4;
+    const int tile = blockIdx.x;
+    const int id = lane < a.n ? a.ids[lane] : -1;
+    int expert;
+    const uint64_t m = same_expert(id, (uint32_t)id < (uint32_t)a.experts, blockIdx.y, expert);
+    if (!m) return;
+    const int n = __popcll(m), pitch = few_pitch(a.hidden);
+    const uint32_t blocks = a.hidden / 32;
+    const int64_t first = (int64_t)expert * 2 * a.inter + tile * 16;
+    const Tile tiles[2] = {tile_of<F>(a.w13, a.s13, first, a.hidden), tile_of<F>(a.w13, a.s13, first + a.inter, a.hidden)};
+    const uint8_t *const end = scales_end<F>(a.s13, a, 2 * a.inter, a.hidden);
+    for (int g = 0; g < n; g += slots) {
+        const int count = min(slots, n - g);
+        f32x4 acc[2] = {};
+        for (uint32_t start = 0; start < blocks; start += kSpan<F> / 32) {
+            const uint32_t here = min(blocks - start, (uint32_t)kSpan<F> / 32);
+            const uint8_t *x = xs + min(row, count - 1) * pitch + (start + quarter) * 64;
+            const auto stage_x = [&](const auto &then) {
+                if (start == 0)
+                    stage<kGateWaves, 2>(
+                        xs, count, a.hidden,
+                        [&](int c) { return a.x + (int64_t)(nth_bit(m, g + c) / a.top) * a.xs; }, then);
+                else then();
+            };
+            constexpr int kMost = kSpan<F> / 256 / kGateWaves;
+            if (here <= 16 * kGateWaves / 2 * (kMost / 2))
+                gate_up_span<F, kMost / 2>(scales, tiles, end, blocks, start, here, x, stage_x, acc);
+            else gate_up_span<F, kMost>(scales, tiles, end, blocks, start, here, x, stage_x, acc);
+            if (start + kSpan<F> / 32 < blocks) __syncthreads();  // the scales are read
+        }
+        if (row < count)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) *reinterpret_cast<f32x4 *>(&joined[wave][i][row][quarter * 4]) = acc[i];
+        __syncthreads();
+        const float f = F == NV ? a.f13[expert] : 1.0f;
+        if ((int)threadIdx.x < count * 16) {
+            const int c = threadIdx.x / 16, r = threadIdx.x % 16;
+            float gate = 0.0f, up = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kGateWaves; ++j) gate += joined[j][0][c][r], up += joined[j][1][c][r];
+            const int64_t to = (int64_t)nth_bit(m, g + c) * a.inter + tile * 16 + r;
+            split(silu(gate * f) * (up * f), a.hi[to], a.lo[to]);
+        }
+        __syncthreads();
+    }
+}
+
+// 16 output rows of all assignments. An item is an expert and a part of k (so that the
+// waves have work where experts are fewer); its h lies in LDS, put there by the wave that
+// needs it. Columns 0 .. 7 are the upper halves of the expert's h, 8 .. 15 the rests. An
+// item's results, weighted, go to LDS, one place for each (part, assignment), and are
+// added in a fixed order.
+constexpr int kDownWaves = 16, kDownBatch = 3, kPlaces = 128;
+
+template <int F>
+__global__ __launch_bounds__(kDownWaves * 64) void k_down_few(Args a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t hs[];
+    __shared__ __attribute__((aligned(16))) float part[kPlaces][16];
+    __shared__ float factor[kFew];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15,
+              quarter = lane >> 4;
+    const int id = lane < a.n ? a.ids[lane] : -1;
+    const bool valid = (uint32_t)id < (uint32_t)a.experts;
+    const float weight = lane < a.n ? a.weights[lane] : 0.0f;  // lane: an assignment
+    const int blocks = a.inter / 32, pairs = (blocks + 7) / 8, pitch = few_pitch(a.inter);
+    int before = kFew;  // the first lane with this one's expert; a leader is its own
+    for (int i0 = (a.n - 1) / 8 * 8; i0 >= 0; i0 -= 8)
+#pragma unroll
+        for (int i = 7; i >= 0; --i)
+            if (__builtin_amdgcn_readlane(id, i0 + i) == id) before = i0 + i;
+    const uint64_t leaders = __ballot(valid && before == lane);
+    const int found = __popcll(leaders);
+    int parts = 1;
+    if (found > 0) parts = max(1, min(min(kDownWaves / found, kPlaces / a.n), pairs));
+    const int items = found * parts;
+    struct Item {
+        uint64_t m;  // its assignments
+        int p;       // its part: pairs p, p + parts, ...
+        Tile tiles[1];
+        u32x4 h[kDownBatch];  // of the first assignment
+        Batch<F, 1, kDownBatch> batch;
+    };
+    // Pairs t, t + parts, ... of an assignment's h: lanes 0 .. 31 the upper halves, the others the rests.
+    const auto load_h = [&](u32x4 (&h)[kDownBatch], int at, int t) {
+        const uint16_t *from = (lane < 32 ? a.hi : a.lo) + (int64_t)at * a.inter;
+#pragma unroll
+        for (int u = 0; u < kDownBatch; ++u) {
+            const int k = (t + u * parts) * 256 + (lane & 31) * 8;
+            h[u] = ld16(from + (k < a.inter ? k : 0));
+            if (k >= a.inter) h[u] = u32x4{0, 0, 0, 0};
+        }
+    };
+    const auto store_h = [&](const u32x4 (&h)[kDownBatch], int at, int t) {
+#pragma unroll
+        for (int u = 0; u < kDownBatch; ++u)
+            if (t + u * parts < pairs)
+                *reinterpret_cast<u32x4 *>(hs + (2 * at + (lane >> 5)) * pitch + (t + u * parts) * 512 + (lane & 31) * 16) = h[u];
+    };
+    const auto begin = [&](Item &it, int item) {
+        int expert;
+        it.m = same_expert(id, valid, nth_bit(leaders, item % found), expert);
+        it.p = item / found;
+        it.tiles[0] = tile_of<F>(a.w2, a.s2, (int64_t)expert * a.hidden + blockIdx.x * 16, a.inter);
+        load_h(it.h, nth_bit(it.m, 0), it.p);
+        it.batch.load(it.tiles, blocks, it.p, parts);
+        fix();
+    };
+    Item it;
+    if (wave < items) begin(it, wave);
+    if (wave == 0) factor[lane] = valid ? weight * (F == NV ? a.f2[id] : 1.0f) : 0.0f;
+    for (int item = wave; item < items; item += kDownWaves) {
+        const int n = __popcll(it.m);
+        Item next;
+        if (item + kDownWaves < items) begin(next, item + kDownWaves);
+        for (int g = 0; g < n; g += 8) {
+            const int at = nth_bit(it.m, min(g + (row & 7), n - 1));
+            const uint8_t *x = hs + (2 * at + (row >> 3)) * pitch + quarter * 64;
+            f32x4 acc[1] = {};
+            for (int t = it.p; t < pairs; t += parts * kDownBatch) {
+                if (t != it.p || g) it.batch.load(it.tiles, blocks, t, parts);
+                if (g == 0)
+                    for (int c = 0; c < n; ++c) {
+                        if (t != it.p || c) load_h(it.h, nth_bit(it.m, c), t);
+                        store_h(it.h, nth_bit(it.m, c), t);
+                    }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                it.batch.multiply(x, pairs, t, parts, acc);
+            }
+            f32x4 v = acc[0];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += dpp_f32<0x128>(v[i]);  // row_ror:8: the rest's column
+            if (row < 8 && g + row < n) *reinterpret_cast<f32x4 *>(&part[it.p * a.n + at][quarter * 4]) = v;
+        }
+        if (item + kDownWaves < items) it = next;
+    }
+    __syncthreads();
+    const uint64_t all = __ballot(valid);
+    for (int i = threadIdx.x; i < a.tokens * 16; i += kDownWaves * 64) {
+        const int t = i / 16, r = i % 16;
+        float v = 0.0f;
+        for (int j0 = 0; j0 < a.top; j0 += 8) {
+            float y[8] = {};
+            for (int p = 0; p < parts; ++p)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] += part[p * a.n + t * a.top + min(j0 + j, a.top - 1)][r];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = t * a.top + min(j0 + j, a.top - 1);
+                if (j0 + j < a.top && all >> at & 1) v += y[j] * factor[at];
+            }
+        }
+        a.out[t * a.os + blockIdx.x * 16 + r] = bf16_bits_rne(v);
+    }
+}
+
+// ---------------------------------------------------------------- more tokens
+//
+// A workgroup's waves have 16 gate and 16 up rows (or 32 output rows) each, over all
+// of k, and the same columns. Columns come through LDS, 256 elements of each at a
+// time, two such pieces in turn; they are loaded into registers two pieces ahead, so
+// that the barrier between two pieces waits for no load that is younger than the
+// weights it is multiplied with. Weights are loaded one piece ahead, a line at a time
+// (its two halves one after the other: apart, each would ask the second cache for it);
+// their scales, of which a piece has only 8 bytes a row, come into LDS first, kSpan
+// elements' at a time.
+constexpr int kWaves = 8, kTiles = 4;  // tiles: of 16 columns, at most at a time
+struct Shared {
+    u32x4 x[2][kTiles][32][16];
+    uint8_t scales[kWaves][32][kScalePitch];
+};
+
+// acc[i][m] += 16 rows x 16 columns of (tile i, columns' tile m), over the span of k
+// from `start` on. column(m, c): where column c of tile m lies.
+//
+// In LDS the columns' 16-byte parts lie part by part, a tile's 16 columns side by side
+// in the order column ^ part: writes (32 parts of a column) and reads (16 columns of a
+// part) both go through all banks.
+template <int F, int XT, typename C>
+__device__ __forceinline__ void stream(Shared &lds, const Tile (&tiles)[2], const uint8_t *end, const C &column, int k, int start,
+                                       f32x4 (&acc)[2][XT]) {
+    const uint32_t lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t blocks = k / 32, first = start / 32, count = min(blocks - first, (uint32_t)kSpan<F> / 32);
+    const int pairs = (count + 7) / 8;
+    uint8_t *const scales = &lds.scales[wave][0][0];
+    copy_scales<F, 1>(scales, tiles, end, blocks, first, count, [] {});
+    fix();
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): from here on the compiler can count what is in flight
+    // this thread's part of a piece, of a column of each tile
+    const int part = threadIdx.x & 31, c = threadIdx.x >> 5;
+    const uint16_t *x[XT];
+#pragma unroll
+    for (int i = 0; i < XT; ++i) x[i] = column(i, c) + start;
+    u32x4 xr[2][XT], p[2][2][2];
+    const auto load_x = [&](u32x4 (&v)[XT], int d) {
+        const bool in = d * 32 + part < (int)count * 4;
+#pragma unroll
+        for (int i = 0; i < XT; ++i) {
+            v[i] = ld16(x[i] + (in ? d * 256 + part * 8 : 0));
+            if (!in) v[i] = u32x4{0, 0, 0, 0};  // beyond the span
+        }
+    };
+    const auto store_x = [&](const u32x4 (&v)[XT], int buf) {
+#pragma unroll
+        for (int i = 0; i < XT; ++i)
+            lds.x[buf][i][part][c ^ (part & 15)] = v[i];
+    };
+    const uint32_t row_at = row * blocks + first;
+    const auto load_w = [&](u32x4 (&q)[2][2], uint32_t d) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                q[h][i] = ld16(tiles[i].w + (row_at + min(8 * d + 4 * h + quarter, count - 1)) * 16);
+    };
+    load_x(xr[0], 0);
+    fix();
+    load_x(xr[1], 1);
+    fix();
+    load_w(p[0], 0);
+    fix();
+    store_x(xr[0], 0);
+    lds_barrier();
+    for (int d0 = 0;; d0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int d = d0 + u;
+            if (d >= pairs) goto done;
+            load_x(xr[u], d + 2);
+            fix();
+            load_w(p[u ^ 1], d + 1);
+            fix();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t scale[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    scale[i] = scale_of<F>(scales, i * 16 + row, min(8 * d + 4 * h + quarter, count - 1));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = (h * 4 + quarter) * 4 + j;
+                    bf16x8 v[XT];
+#pragma unroll
+                    for (int m = 0; m < XT; ++m) v[m] = kv::as_bf16x8(lds.x[u][m][at][row ^ (at & 15)]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bf16x8 e = expand<F>(p[u][h][i][j], scale[i], j);
+#pragma unroll
+                        for (int m = 0; m < XT; ++m)
+                            acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e, v[m], acc[i][m], 0, 0, 0);
+                    }
+                }
+            }
+            fix();
+            store_x(xr[u ^ 1], u ^ 1);
+            lds_barrier();
+        }
+    }
+done:;
+}
+
+template <int F, int XT>
+__device__ __forceinline__ void gate_up(const Args &a, Shared &lds, int tile, int expert, int n, const int *list) {
+    const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
+    const bool mine = tile < a.inter / 16;
+    const int at = min(tile, a.inter / 16 - 1) * 16;
+    const int64_t first = (int64_t)expert * 2 * a.inter + at;
+    const Tile tiles[2] = {tile_of<F>(a.w13, a.s13, first, a.hidden), tile_of<F>(a.w13, a.s13, first + a.inter, a.hidden)};
+    const auto column = [&](int m, int c) { return a.x + (int64_t)(list[min(16 * m + c, n - 1)] / a.top) * a.xs; };
+    f32x4 acc[2][XT] = {};
+    const uint8_t *const end = scales_end<F>(a.s13, a, 2 * a.inter, a.hidden);
+    for (int k = 0; k < a.hidden; k += kSpan<F>) stream<F, XT>(lds, tiles, end, column, a.hidden, k, acc);
+    const float f = F == NV ? a.f13[expert] : 1.0f;
+#pragma unroll
+    for (int m = 0; m < XT; ++m) {
+        if (!mine || 16 * m + row >= n) continue;
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split(silu(acc[0][m][i] * f) * (acc[1][m][i] * f), hi[i], lo[i]);
+        const int64_t to = (int64_t)list[16 * m + row] * a.inter + at + quarter * 4;
+        *reinterpret_cast<u32x2 *>(a.hi + to) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+        *reinterpret_cast<u32x2 *>(a.lo + to) = u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+    }
+}
+
+// The columns are h's upper halves and its rests: eight of each in one tile, or the
+// tiles of the one and then those of the other. Either way their sums are added at the end, so that
+// no result depends on which assignments come together.
+template <int F, int XT>
+__device__ __forceinline__ void down(const Args &a, Shared &lds, int tile, int expert, int n, const int *list) {
+    const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
+    const bool mine = tile < a.hidden / 32;
+    const int at = min(tile, a.hidden / 32 - 1) * 32;
+    const int64_t first = (int64_t)expert * a.hidden + at;
+    const Tile tiles[2] = {tile_of<F>(a.w2, a.s2, first, a.inter), tile_of<F>(a.w2, a.s2, first + 16, a.inter)};
+    const auto column = [&](int m, int c) {
+        const int at = 16 * m + c, half = 8 * XT;
+        return (at < half ? a.hi : a.lo) + (int64_t)list[min(at % half, n - 1)] * a.inter;
+    };
+    constexpr int OUT = XT > 1 ? XT / 2 : 1;
+    int to[OUT];
+    float weight[OUT];
+#pragma unroll
+    for (int m = 0; m < OUT; ++m) {
+        to[m] = list[min(16 * m + row, n - 1)];
+        weight[m] = a.weights[to[m]] * (F == NV ? a.f2[expert] : 1.0f);
+    }
+    f32x4 acc[2][XT] = {};
+    const uint8_t *const end = scales_end<F>(a.s2, a, a.hidden, a.inter);
+    for (int k = 0; k < a.inter; k += kSpan<F>) stream<F, XT>(lds, tiles, end, column, a.inter, k, acc);
+#pragma unroll
+    for (int m = 0; m < OUT; ++m) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc[i][m][r] += XT > 1 ? acc[i][(m + OUT) % XT][r] : dpp_f32<0x128>(acc[i][m][r]);  // row_ror:8
+        if (!mine || 16 * m + row >= n || (XT == 1 && row >= 8)) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<f32x4 *>(a.y + (int64_t)to[m] * a.hidden + at + i * 16 + quarter * 4) = acc[i][m] * weight[m];
+    }
+}
+
+template <int F, bool DOWN>
+__global__ __launch_bounds__(kWaves * 64) void k_stream(Args a) {
+    __shared__ Shared lds;
+    const int4 slot = a.slots[blockIdx.y];
+    const int expert = slot.x;
+    if (expert < 0) return;
+    const int tile = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int *list = a.list + slot.y;
+    int n = slot.z;
+    constexpr int EACH = DOWN ? 8 : 16;  // assignments that a tile of columns holds
+    for (; n > 0; n -= EACH * kTiles, list += EACH * kTiles) {
+        const int now = min(n, EACH * kTiles);
+        if constexpr (DOWN) {
+            if (now <= EACH) down<F, 1>(a, lds, tile, expert, now, list);
+            else if (now <= 2 * EACH) down<F, 2>(a, lds, tile, expert, now, list);
+            else down<F, 4>(a, lds, tile, expert, now, list);
+        } else {
+            if (now <= EACH) gate_up<F, 1>(a, lds, tile, expert, now, list);
+            else if (now <= 2 * EACH) gate_up<F, 2>(a, lds, tile, expert, now, list);
+            else gate_up<F, 4>(a, lds, tile, expert, now, list);
+        }
     }
 }
 
@@ -310,78 +663,10 @@ __global__ __launch_bounds__(256) void k_add(Args a) {
     }
 }
 
-// Few assignments: 16 output rows of all of them. An item is an expert and a part of k
-// (so that eight waves have work where experts are fewer); its results, weighted, go
-// to LDS, one place for each (part, assignment), and are added in a fixed order.
-template <int F, int MT>
-__device__ __forceinline__ void down_item(const Args &a, float *part, const int *cols, int n, int expert, int first,
-                                          int every) {
-    const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
-    constexpr int SB = F == MX ? 32 : 16;
-    const int64_t r = (int64_t)expert * a.hidden + blockIdx.x * 16 + row;
-    const uint8_t *w[1] = {a.w2 + r * (a.inter / 2)}, *s[1] = {a.s2 + r * (a.inter / SB)};
-    const uint16_t *x[MT], *xl[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t at = (int64_t)cols[min(16 * m + row, n - 1)] * a.inter;
-        x[m] = a.hi + at, xl[m] = a.lo + at;
-    }
-    f32x4 acc[1][MT] = {};
-    products<F, 1, MT, true>(w, s, x, xl, a.inter, first, every, acc);
-    const float f = F == NV ? a.f2[expert] : 1.0f;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-        if (16 * m + row < n) {
-            const int at = cols[16 * m + row];
-            *reinterpret_cast<f32x4 *>(part + at * 16 + quarter * 4) = acc[0][m] * (a.weights[at] * f);
-        }
-}
-
-constexpr int kDownWaves = 8;
-
-template <int F>
-__global__ __launch_bounds__(kDownWaves * 64) void k_down_few(Args a) {
-    __shared__ __attribute__((aligned(16))) float part[kDownWaves * kFew * 16];
-    __shared__ int cols[kDownWaves][kFew];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int id = lane < a.n ? a.ids[lane] : -1;
-    const bool valid = (uint32_t)id < (uint32_t)a.experts;
-    int found = 0, expert;
-    for (int i = 0; i < a.n; ++i) found += same_expert(id, valid, i, expert) != 0;
-    const int parts = found > 0 && found < kDownWaves ? kDownWaves / found : 1;
-    for (int item = wave; item < found * parts; item += kDownWaves) {
-        const int p = item / found;
-        int left = item - p * found, slot = -1;
-        uint64_t m = 0;
-        for (int i = 0; i < a.n && left >= 0; ++i)
-            if ((m = same_expert(id, valid, i, expert)) != 0) --left, slot = i;
-        m = same_expert(id, valid, slot, expert);
-        if (m >> lane & 1) cols[wave][__popcll(m & (((uint64_t)1 << lane) - 1))] = lane;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const int n = __popcll(m);
-        if (n <= 16) down_item<F, 1>(a, part + p * a.n * 16, cols[wave], n, expert, p, parts);
-        else down_item<F, 4>(a, part + p * a.n * 16, cols[wave], n, expert, p, parts);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.tokens * 16; i += kDownWaves * 64) {
-        const int t = i / 16, row = i % 16;
-        float v = 0.0f;
-        for (int j = 0; j < a.top; ++j) {
-            const int at = t * a.top + j;
-            if ((uint32_t)a.ids[at] >= (uint32_t)a.experts) continue;
-            float y = 0.0f;
-            for (int p = 0; p < parts; ++p) y += part[(p * a.n + at) * 16 + row];
-            v += y;
-        }
-        a.out[t * a.os + blockIdx.x * 16 + row] = bf16_bits_rne(v);
-    }
-}
-
 // Many assignments: lists by expert, and the experts that have any (then -1). One
 // workgroup. The order within an expert's list is left open: no result depends on it.
 constexpr int kListThreads = 1024;
-__global__ __launch_bounds__(kListThreads) void k_lists(Args a, int32_t *list, int32_t *start, int32_t *active) {
+__global__ __launch_bounds__(kListThreads) void k_lists(Args a, int32_t *list, int4 *slots) {
     __shared__ int count[1024], at[1024];
     __shared__ int64_t scan[kListThreads / 64 + 1];
     const int e = threadIdx.x;
@@ -397,11 +682,8 @@ __global__ __launch_bounds__(kListThreads) void k_lists(Args a, int32_t *list, i
     // both sums at once: assignments below, experts with any above
     const int64_t before = kv::block_scan<kListThreads>((int64_t)mine | (int64_t)(mine > 0) << 32, scan, total);
     at[e] = (int)(uint32_t)before;
-    if (e < a.experts) start[e] = (int)(uint32_t)before;
-    if (e == 0) start[a.experts] = (int)(uint32_t)total;
-    if (mine > 0) active[before >> 32] = e;
-    const int slots = min(a.n, a.experts);
-    if (e < slots && e >= (int)(total >> 32)) active[e] = -1;
+    if (mine > 0) slots[before >> 32] = make_int4(e, (int)(uint32_t)before, mine, 0);
+    if (e < min(a.n, a.experts) && e >= (int)(total >> 32)) slots[e] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     for (int i = threadIdx.x; i < a.n; i += kListThreads) {
         const uint32_t id = (uint32_t)a.ids[i];
@@ -409,33 +691,41 @@ __global__ __launch_bounds__(kListThreads) void k_lists(Args a, int32_t *list, i
     }
 }
 
+// The form for few tokens, where x and h fit LDS.
+constexpr int kFewLds = 128 << 10;
+bool is_few(const qbn_moe_weights &e, int64_t tokens, int top) {
+    return tokens <= kFewTokens && tokens * top <= kFew && few_pitch(e.hidden) <= kFewLds &&
+           tokens * top * 2 * few_pitch(e.inter) <= kFewLds;
+}
+
 struct Layout {  // of the workspace, in bytes
-    int64_t hi, lo, y, list, start, active, end;
+    int64_t hi, lo, y, slots, list, end;
 };
 Layout layout_of(const qbn_moe_weights &e, int64_t tokens, int top) {
     const int64_t n = (tokens < QBN_MOE_PORTION ? tokens : QBN_MOE_PORTION) * top;
-    const bool few = n <= kFew;
+    const bool few = is_few(e, tokens, top);
     Layout l;
     l.hi = 0;
     l.lo = l.hi + n * e.inter * 2;
     l.y = l.lo + n * e.inter * 2;
-    l.list = l.y + (few ? 0 : n * e.hidden * 4);
-    l.start = l.list + (few ? 0 : n * 4);
-    l.active = l.start + (few ? 0 : (e.experts + 1) * 4);
-    l.end = l.active + (few ? 0 : e.experts * 4);
+    l.slots = l.y + (few ? 0 : n * e.hidden * 4);
+    l.list = l.slots + (few ? 0 : e.experts * (int64_t)sizeof(int4));
+    l.end = l.list + (few ? 0 : n * 4);
     return l;
 }
 
 template <int F>
-hipError_t launch(const Args &a, int32_t *list, int32_t *start, int32_t *active, hipStream_t s) {
-    if (a.n <= kFew) {
-        k_gate_up<F, true><<<dim3(a.inter / 16, a.n), 256, 0, s>>>(a);
-        k_down_few<F><<<a.hidden / 16, kDownWaves * 64, 0, s>>>(a);
+hipError_t launch(const Args &a, bool few, int32_t *list, int4 *where, hipStream_t s) {
+    if (few) {
+        const int pitch = few_pitch(a.hidden), slots = a.tokens < kFewLds / pitch ? a.tokens : kFewLds / pitch;
+        const dim3 grid(a.inter / 16, a.n);
+        k_gate_up_few<F><<<grid, kGateWaves * 64, slots * pitch, s>>>(a, slots);
+        k_down_few<F><<<a.hidden / 16, kDownWaves * 64, 2 * a.n * few_pitch(a.inter), s>>>(a);
     } else {
         const int slots = a.n < a.experts ? a.n : a.experts;
-        k_lists<<<1, kListThreads, 0, s>>>(a, list, start, active);
-        k_gate_up<F, false><<<dim3(a.inter / 16, slots), 256, 0, s>>>(a);
-        k_down<F><<<dim3(a.hidden / 32, slots), 256, 0, s>>>(a);
+        k_lists<<<1, kListThreads, 0, s>>>(a, list, where);
+        k_stream<F, false><<<dim3((a.inter / 16 + kWaves - 1) / kWaves, slots), kWaves * 64, 0, s>>>(a);
+        k_stream<F, true><<<dim3((a.hidden / 32 + kWaves - 1) / kWaves, slots), kWaves * 64, 0, s>>>(a);
         const int64_t blocks = ((int64_t)a.tokens * (a.hidden / 8) + 255) / 256;
         k_add<<<(unsigned)blocks, 256, 0, s>>>(a);
     }
@@ -453,19 +743,21 @@ hipError_t launch_moe_experts(const qbn_moe_weights &e, int64_t tokens, int top_
                               hipStream_t s) {
     const Layout l = layout_of(e, tokens, top_k);
     uint8_t *b = (uint8_t *)ws;
+    Args a = {};
+    a.w13 = (const uint8_t *)e.w13, a.s13 = (const uint8_t *)e.w13_scales, a.f13 = e.w13_scale2;
+    a.w2 = (const uint8_t *)e.w2, a.s2 = (const uint8_t *)e.w2_scales, a.f2 = e.w2_scale2;
+    a.xs = x_stride, a.os = out_stride;
+    a.top = top_k, a.experts = e.experts, a.hidden = e.hidden, a.inter = e.inter;
+    a.hi = (uint16_t *)(b + l.hi), a.lo = (uint16_t *)(b + l.lo), a.y = (float *)(b + l.y);
+    int32_t *list = (int32_t *)(b + l.list);
+    int4 *slots = (int4 *)(b + l.slots);
+    a.list = list, a.slots = slots;
     for (int64_t at = 0; at < tokens; at += QBN_MOE_PORTION) {
-        Args a;
-        a.w13 = (const uint8_t *)e.w13, a.s13 = (const uint8_t *)e.w13_scales, a.f13 = e.w13_scale2;
-        a.w2 = (const uint8_t *)e.w2, a.s2 = (const uint8_t *)e.w2_scales, a.f2 = e.w2_scale2;
-        a.x = (const uint16_t *)x + at * x_stride, a.xs = x_stride;
-        a.out = (uint16_t *)out + at * out_stride, a.os = out_stride;
+        a.tokens = (int)(tokens - at < QBN_MOE_PORTION ? tokens - at : QBN_MOE_PORTION), a.n = a.tokens * top_k;
+        a.x = (const uint16_t *)x + at * x_stride, a.out = (uint16_t *)out + at * out_stride;
         a.ids = ids + at * top_k, a.weights = weights + at * top_k;
-        a.hi = (uint16_t *)(b + l.hi), a.lo = (uint16_t *)(b + l.lo), a.y = (float *)(b + l.y);
-        a.list = (int32_t *)(b + l.list), a.start = (int32_t *)(b + l.start), a.active = (int32_t *)(b + l.active);
-        a.tokens = (int)(tokens - at < QBN_MOE_PORTION ? tokens - at : QBN_MOE_PORTION);
-        a.top = top_k, a.n = a.tokens * top_k, a.experts = e.experts, a.hidden = e.hidden, a.inter = e.inter;
-        int32_t *list = (int32_t *)(b + l.list), *start = (int32_t *)(b + l.start), *active = (int32_t *)(b + l.active);
-        const hipError_t st = e.format == QBN_MXFP4 ? launch<MX>(a, list, start, active, s) : launch<NV>(a, list, start, active, s);
+        const bool few = is_few(e, a.tokens, top_k);
+        const hipError_t st = e.format == QBN_MXFP4 ? launch<MX>(a, few, list, slots, s) : launch<NV>(a, few, list, slots, s);
         if (st != hipSuccess) return st;
     }
     return hipSuccess;

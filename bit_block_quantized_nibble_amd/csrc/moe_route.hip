@@ -9,9 +9,10 @@
 // token's; bound by latency. More: 16 tokens by 16 experts a workgroup on the
 // matrix cores, k split over its waves; bound by binary64 products from about 100
 // tokens on. Then a wave per token finds the best one after the other.
-#include "kv_device.h"
 #include "moe_launch.h"
 #include "rope_device.h"
+
+#include <algorithm>
 
 namespace qbn {
 namespace {
@@ -20,15 +21,16 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 constexpr int64_t kPortion = 4096;  // tokens whose logits the workspace holds at a time
 constexpr int kFew = 4;             // tokens of the vector form
+constexpr int64_t kParts = 8;       // of the hidden size, at most
 
 struct Args {
     const __bf16 *x, *w;
+    double *logits;  // [parts][tokens][experts], without the bias
     const float *bias;
-    double *logits;  // [tokens][experts]
     int32_t *ids;
     float *weights;
     int64_t xs;
-    int tokens, experts, hidden, top, normalize;
+    int tokens, experts, hidden, top, normalize, parts;
 };
 
 // The sum over a wave's lanes, in all of them.
@@ -36,6 +38,37 @@ __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
     return v;
+}
+
+// Numbers as unsigned words of the same order, all of them above 0; NaN as -inf.
+__device__ __forceinline__ uint64_t ordered(double v) {
+    if (v != v) v = -__builtin_huge_val();
+    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 is 0
+    return b ^ (b >> 63 ? ~(uint64_t)0 : (uint64_t)1 << 63);
+}
+__device__ __forceinline__ double number(uint64_t b) {
+    return __builtin_bit_cast(double, b ^ (b >> 63 ? (uint64_t)1 << 63 : ~(uint64_t)0));
+}
+
+// The largest over a wave's lanes, the same in all of them.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    const auto step = [](uint32_t x, int y) { return max(x, (uint32_t)y); };
+    v = step(v, kv::dpp_i32<0x111, 0xF>((int)v));  // shifts within rows of 16, then rows into the next
+    v = step(v, kv::dpp_i32<0x112, 0xF>((int)v));  // (lanes without a source read 0)
+    v = step(v, kv::dpp_i32<0x114, 0xF>((int)v));
+    v = step(v, kv::dpp_i32<0x118, 0xF>((int)v));
+    v = step(v, kv::dpp_i32<0x142, 0xA>((int)v));
+    v = step(v, kv::dpp_i32<0x143, 0xC>((int)v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// Of words of 64 bits: their upper halves decide, and where several lanes have the largest, the lower.
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    const uint32_t hi = wave_max((uint32_t)(v >> 32));
+    const bool mine = (uint32_t)(v >> 32) == hi;
+    const uint64_t m = __ballot(mine);
+    const uint32_t lo = m & (m - 1) ? wave_max(mine ? (uint32_t)v : 0)
+                                    : (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, __builtin_ctzll(m));
+    return (uint64_t)hi << 32 | lo;
 }
 
 template <int T>
@@ -60,15 +93,14 @@ __global__ __launch_bounds__(256) void k_logits_few(Args a) {
     }
     __syncthreads();
     if ((int)threadIdx.x < T && (int)threadIdx.x < a.tokens) {
-        double s = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
-        if (a.bias) s += (double)a.bias[e];
-        a.logits[(int64_t)threadIdx.x * a.experts + e] = s;
+        a.logits[(int64_t)threadIdx.x * a.experts + e] =
+            (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
     }
 }
 
 // 16 tokens x 16 experts. A wave's k come in pieces of 32, of which the lanes of a
 // quarter (16 lanes) have eight in a row each: which k a product step takes is
-// free, as long as both operands agree.
+// free, as long as both operands agree. Of a part of k: blockIdx.y.
 template <int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void k_logits(Args a) {
     __shared__ double part[WAVES][256];
@@ -78,7 +110,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_logits(Args a) {
     const __bf16 *x = a.x + (int64_t)min(t0 + row, a.tokens - 1) * a.xs + quarter * 8;
     const __bf16 *w = a.w + (int64_t)min(e0 + row, a.experts - 1) * a.hidden + quarter * 8;
     f64x4 acc = {0, 0, 0, 0};
-    for (int k = wave * 32; k < a.hidden; k += WAVES * 32) {
+    for (int k = (wave * a.parts + blockIdx.y) * 32; k < a.hidden; k += WAVES * a.parts * 32) {
         float u[8], v[8];
         rope::floats(rope::load8(x + k), u);
         rope::floats(rope::load8(w + k), v);
@@ -93,72 +125,43 @@ __global__ __launch_bounds__(WAVES * 64) void k_logits(Args a) {
 #pragma unroll
         for (int j = 0; j < WAVES; ++j) s += part[j][i];
         const int t = t0 + i / 16, e = e0 + i % 16;
-        if (t < a.tokens && e < a.experts) {
-            if (a.bias) s += (double)a.bias[e];
-            a.logits[(int64_t)t * a.experts + e] = s;
-        }
+        if (t < a.tokens && e < a.experts) a.logits[((int64_t)blockIdx.y * a.tokens + t) * a.experts + e] = s;
     }
 }
 
-// Numbers as unsigned words of the same order, all of them above 0; NaN as -inf.
-__device__ __forceinline__ uint64_t ordered(double v) {
-    if (v != v) v = -__builtin_huge_val();
-    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 is 0
-    return b ^ (b >> 63 ? ~(uint64_t)0 : (uint64_t)1 << 63);
-}
-__device__ __forceinline__ double number(uint64_t b) {
-    return __builtin_bit_cast(double, b ^ (b >> 63 ? (uint64_t)1 << 63 : ~(uint64_t)0));
-}
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint64_t max_dpp(uint64_t v) {
-    const uint64_t o = (uint64_t)(uint32_t)kv::dpp_i32<CTRL, ROWS>((int)(uint32_t)v) |
-                       (uint64_t)(uint32_t)kv::dpp_i32<CTRL, ROWS>((int)(uint32_t)(v >> 32)) << 32;
-    return o > v ? o : v;
-}
-// The largest over a wave's lanes, the same in all of them.
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-    v = max_dpp<0x111, 0xF>(v);  // shifts within rows of 16, then rows into the next (lanes without a source read 0)
-    v = max_dpp<0x112, 0xF>(v);
-    v = max_dpp<0x114, 0xF>(v);
-    v = max_dpp<0x118, 0xF>(v);
-    v = max_dpp<0x142, 0xA>(v);
-    v = max_dpp<0x143, 0xC>(v);
-    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63) |
-           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63) << 32;
-}
-
-// A wave per token; lane l has experts l, l + 64, ... (EACH of them).
+// A wave per token; lane l looks at experts l, l + 64, ... (EACH of them).
 template <int EACH>
 __global__ __launch_bounds__(256) void k_choose(Args a) {
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (t >= a.tokens) return;
     uint64_t key[EACH];
-    double total = 0.0;
+    double v[EACH];
     bool nan = false;
 #pragma unroll
+    for (int j = 0; j < EACH; ++j) v[j] = a.bias ? (double)a.bias[min(lane + 64 * j, a.experts - 1)] : 0.0;
+    constexpr int AHEAD = EACH <= 4 ? 8 : 2;  // loads sent together: one after another, they cost a microsecond each
+    for (int p0 = 0; p0 < a.parts; p0 += AHEAD) {
+        double u[AHEAD][EACH];
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+#pragma unroll
+            for (int j = 0; j < EACH; ++j)
+                u[p][j] = a.logits[((int64_t)min(p0 + p, a.parts - 1) * a.tokens + t) * a.experts +
+                                   min(lane + 64 * j, a.experts - 1)];
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) v[j] += p0 + p < a.parts ? u[p][j] : 0.0;
+    }
+#pragma unroll
     for (int j = 0; j < EACH; ++j) {
-        const int e = lane + 64 * j;
-        const double v = e < a.experts ? a.logits[(int64_t)t * a.experts + e] : 0.0;
-        key[j] = e < a.experts ? ordered(v) : 0;
-        nan = nan || v != v;
+        key[j] = lane + 64 * j < a.experts ? ordered(v[j]) : 0;
+        nan = nan || v[j] != v[j];
     }
     nan = __ballot(nan) != 0;
-    uint64_t first = key[0];
-#pragma unroll
-    for (int j = 1; j < EACH; ++j) first = key[j] > first ? key[j] : first;
-    first = wave_max(first);
-    const double best = number(first);
-    if (!a.normalize) {
-        double s = 0.0;
-#pragma unroll
-        for (int j = 0; j < EACH; ++j)
-            if (key[j]) s += exp(number(key[j]) - best);
-        total = wave_sum(s);
-    }
-    int id = 0;         // lane j: the j-th expert
-    double mine = 0.0;  // and its logit
+    int id = 0;
+    double mine = 0.0, best = 0.0;  // its logit, and the largest
     for (int r = 0; r < a.top; ++r) {
         uint64_t top = key[0];
 #pragma unroll
@@ -174,8 +177,16 @@ __global__ __launch_bounds__(256) void k_choose(Args a) {
         for (int j = 0; j < EACH; ++j)
             if (e == lane + 64 * j) key[j] = 0;
         if (lane == r) id = e, mine = number(top);
+        if (r == 0) best = number(top);
     }
-    double p = lane < a.top ? exp(mine - best) : 0.0;
+    double total = 0.0;
+    if (!a.normalize) {
+        double s = 0.0;
+        for (int j = 0; j < EACH; ++j)
+            if (lane + 64 * j < a.experts) s += exp((v[j] != v[j] ? -__builtin_huge_val() : v[j]) - best);
+        total = wave_sum(s);
+    }
+    const double p = lane < a.top ? exp(mine - best) : 0.0;
     if (a.normalize) total = wave_sum(p);
     if (nan) total = __builtin_nan("");
     if (lane < a.top) {
@@ -184,31 +195,44 @@ __global__ __launch_bounds__(256) void k_choose(Args a) {
     }
 }
 
+
+// A binary64 step of 16 x 16 takes 128 cycles of a quarter of a compute unit: where there are fewer
+// such tiles than compute units, k is split over them too, a piece of 32 for each wave at least.
+int parts_of(const qbn_moe_router &r, int64_t tokens) {
+    const int64_t tiles = (tokens + 15) / 16 * ((r.experts + 15) / 16), most = (r.hidden + 511) / 512;
+    const int64_t parts = tokens <= kFew ? 1 : std::min<int64_t>({kParts, 256 / tiles, most});
+    return (int)std::max<int64_t>(parts, 1);
+}
+
 }  // namespace
 
+// No less for more tokens: parts * tiles <= 256 where parts > 1.
 int64_t moe_route_workspace(const qbn_moe_router &r, int64_t tokens) {
-    return 8 * (tokens < kPortion ? tokens : kPortion) * r.experts;
+    const int64_t n = std::min(tokens, kPortion), split = 256 * 16 / ((r.experts + 15) / 16);
+    return 8 * r.experts * std::max(n, std::min(kParts * n, split));
 }
 
 hipError_t launch_moe_route(const qbn_moe_router &r, int64_t tokens, const void *x, int64_t x_stride, int32_t *ids,
                             float *weights, void *ws, hipStream_t s) {
+    Args a = {};
+    a.w = (const __bf16 *)r.weight, a.bias = r.bias, a.logits = (double *)ws, a.xs = x_stride;
+    a.experts = r.experts, a.hidden = r.hidden, a.top = r.top_k, a.normalize = r.normalize;
     for (int64_t at = 0; at < tokens; at += kPortion) {
-        Args a;
-        a.x = (const __bf16 *)x + at * x_stride, a.w = (const __bf16 *)r.weight, a.bias = r.bias;
-        a.logits = (double *)ws, a.ids = ids + at * r.top_k, a.weights = weights + at * r.top_k;
-        a.xs = x_stride, a.tokens = (int)(tokens - at < kPortion ? tokens - at : kPortion);
-        a.experts = r.experts, a.hidden = r.hidden, a.top = r.top_k, a.normalize = r.normalize;
+        a.tokens = (int)std::min(tokens - at, kPortion), a.parts = parts_of(r, a.tokens);
+        a.x = (const __bf16 *)x + at * x_stride, a.ids = ids + at * r.top_k, a.weights = weights + at * r.top_k;
         if (a.tokens <= kFew) {
             (a.tokens == 1 ? k_logits_few<1> : a.tokens == 2 ? k_logits_few<2> : k_logits_few<4>)<<<r.experts, 256, 0, s>>>(a);
         } else {
-            const int tiles = (a.tokens + 15) / 16 * ((r.experts + 15) / 16);
-            if (tiles < 256) k_logits<16><<<tiles, 1024, 0, s>>>(a);
+            const int tiles = (a.tokens + 15) / 16 * ((a.experts + 15) / 16);
+            if (tiles < 256) k_logits<16><<<dim3(tiles, a.parts), 1024, 0, s>>>(a);
             else k_logits<8><<<tiles, 512, 0, s>>>(a);
         }
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
         const int blocks = (a.tokens + 3) / 4, each = (r.experts + 63) / 64;
         (each <= 1 ? k_choose<1> : each <= 2 ? k_choose<2> : each <= 4 ? k_choose<4> : each <= 8 ? k_choose<8> : k_choose<16>)
             <<<blocks, 256, 0, s>>>(a);
-        const hipError_t e = hipGetLastError();
+        e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
