@@ -21,6 +21,8 @@
 #include "kv_device.h"
 #include "moe_launch.h"
 
+#include <algorithm>
+
 namespace qbn {
 namespace {
 
@@ -126,35 +128,36 @@ template <int F>
 constexpr int kSpan = kScaleBytes * (F == MX ? 32 : 16);  // and their elements
 
 // 16 bytes from s on, at any alignment; those from `end` on read as 0, and no byte there is touched
-// (16 bytes lie before it).
-__device__ __forceinline__ u32x4 ld16_before(const uint8_t *s, const uint8_t *end) {
-    const uint32_t beyond = s > end - 16 ? (uint32_t)(s - (end - 16)) : 0;
+// (16 bytes lie before it). value() waits for them.
+struct Bytes16 {
     u32x4 v;
-    __builtin_memcpy(&v, s - beyond, 16);
-    if (beyond & 8) v = u32x4{v.z, v.w, 0, 0};
-    if (beyond & 4) v = u32x4{v.y, v.z, v.w, 0};
-    return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, beyond), __builtin_amdgcn_alignbyte(v.z, v.y, beyond),
-                 __builtin_amdgcn_alignbyte(v.w, v.z, beyond), __builtin_amdgcn_alignbyte(0, v.w, beyond)};
-}
+    uint32_t beyond;  // bytes that the load lies before s
 
-// `count` blocks' scales, from block `first` on, of two tiles into LDS, by each wave (WAVES 1) or by four
-// together. end: of all scales. then(): called when the loads are on their way and before they are waited for.
-template <int F, int WAVES, typename Then>
+    __device__ __forceinline__ void load(const uint8_t *s, const uint8_t *end) {
+        beyond = s > end - 16 ? (uint32_t)(s - (end - 16)) : 0;
+        __builtin_memcpy(&v, s - beyond, 16);
+    }
+    __device__ __forceinline__ u32x4 value() const {
+        u32x4 o = v;
+        if (beyond & 8) o = u32x4{o.z, o.w, 0, 0};
+        if (beyond & 4) o = u32x4{o.y, o.z, o.w, 0};
+        return u32x4{__builtin_amdgcn_alignbyte(o.y, o.x, beyond), __builtin_amdgcn_alignbyte(o.z, o.y, beyond),
+                     __builtin_amdgcn_alignbyte(o.w, o.z, beyond), __builtin_amdgcn_alignbyte(0, o.w, beyond)};
+    }
+};
+
+// `count` blocks' scales, from block `first` on, of two tiles into LDS by 256 threads. end: of all scales.
+// then(): called when the loads are on their way and before they are waited for.
+template <int F, typename Then>
 __device__ __forceinline__ void copy_scales(uint8_t *lds, const Tile (&tiles)[2], const uint8_t *end, uint32_t blocks,
                                             uint32_t first, uint32_t count, const Then &then) {
-    constexpr int EACH = F == MX ? 1 : 2, LOADS = 4 / WAVES;  // bytes of a block
-    const uint32_t i = threadIdx.x & (64 * WAVES - 1);
-    u32x4 v[LOADS];
-#pragma unroll
-    for (int l = 0; l < LOADS; ++l) {
-        const uint32_t row = (i + l * 64) / 8, at = i % 8 * 16;
-        v[l] = ld16_before((row < 16 ? tiles[0].s : tiles[1].s) + (((row & 15) * blocks + first) * EACH + (at < count * EACH ? at : 0)), end);
-    }
+    constexpr int EACH = F == MX ? 1 : 2;  // bytes of a block
+    const uint32_t row = threadIdx.x / 8, at = threadIdx.x % 8 * 16;
+    Bytes16 v;
+    v.load((row < 16 ? tiles[0].s : tiles[1].s) + (((row & 15) * blocks + first) * EACH + (at < count * EACH ? at : 0)), end);
     fix();
     then();
-#pragma unroll
-    for (int l = 0; l < LOADS; ++l)
-        *reinterpret_cast<u32x4 *>(lds + (i + l * 64) / 8 * kScalePitch + i % 8 * 16) = v[l];
+    *reinterpret_cast<u32x4 *>(lds + row * kScalePitch + at) = v.value();
 }
 // The scale, or both, of a block: row of 32, block of those that LDS has.
 template <int F>
@@ -257,7 +260,7 @@ __device__ __forceinline__ void gate_up_span(uint8_t *scales, const Tile (&tiles
     const uint32_t lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), pairs = (here + 7) / 8;
     u32x4 p[TURNS][2][2];
-    copy_scales<F, kGateWaves>(scales, tiles, end, blocks, start, here, [&] {
+    copy_scales<F>(scales, tiles, end, blocks, start, here, [&] {
         stage_x([&] {
 #pragma unroll
             for (int u = 0; u < TURNS; ++u)
@@ -455,143 +458,206 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down_few(Args a) {
 // ---------------------------------------------------------------- more tokens
 //
 // A workgroup's waves have 16 gate and 16 up rows (or 32 output rows) each, over all
-// of k, and the same columns. Columns come through LDS, 256 elements of each at a
-// time, two such pieces in turn; they are loaded into registers two pieces ahead, so
-// that the barrier between two pieces waits for no load that is younger than the
-// weights it is multiplied with. Weights are loaded one piece ahead, a line at a time
-// (its two halves one after the other: apart, each would ask the second cache for it);
-// their scales, of which a piece has only 8 bytes a row, come into LDS first, kSpan
-// elements' at a time.
+// of k, and the same columns; then the next such rows of the same expert, `turns` times.
+// All its pieces (256 elements of k) are one sequence: the loads of one turn's first
+// pieces go out before the last turn's results are written, so that the start, five loads one
+// after the other, is paid once.
+//
+// Columns come through LDS, a piece at a time, two in turn; they are loaded into registers
+// two pieces ahead, so that the barrier between two pieces waits for no load that is younger
+// than the weights it is multiplied with. Weights are loaded one piece ahead, a line at a
+// time (its two halves one after the other: apart, each would ask the second cache for it);
+// scales as above, but 32 bytes of each row at a time.
 constexpr int kWaves = 8, kTiles = 4;  // tiles: of 16 columns, at most at a time
+constexpr int kScaleTurn = 32;         // bytes of a row's scales at a time
 struct Shared {
     u32x4 x[2][kTiles][32][16];
-    uint8_t scales[kWaves][32][kScalePitch];
+    u32x4 scales[kWaves][32][kScaleTurn / 16 + 1];
 };
 
-// acc[i][m] += 16 rows x 16 columns of (tile i, columns' tile m), over the span of k
-// from `start` on. column(m, c): where column c of tile m lies.
+// For each turn, done(turn, acc): acc[i][m] = 16 rows x 16 columns of (row tile i, columns' tile
+// m). rows(turn): a wave's row tiles. column(m, c): where column c of tile m lies. end: of all
+// scales.
 //
 // In LDS the columns' 16-byte parts lie part by part, a tile's 16 columns side by side
 // in the order column ^ part: writes (32 parts of a column) and reads (16 columns of a
 // part) both go through all banks.
-template <int F, int XT, typename C>
-__device__ __forceinline__ void stream(Shared &lds, const Tile (&tiles)[2], const uint8_t *end, const C &column, int k, int start,
-                                       f32x4 (&acc)[2][XT]) {
+struct Pair {
+    Tile tile[2];
+};
+template <int F, int XT, typename R, typename C, typename D>
+__device__ __forceinline__ void stream(Shared &lds, int turns, const R &rows, const uint8_t *end, const C &column, int k,
+                                       const D &done) {
+    constexpr int EACH = F == MX ? 1 : 2, EVERY = kScaleTurn / EACH / 8;  // bytes of a block; pieces that 32 bytes last
     const uint32_t lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t blocks = k / 32, first = start / 32, count = min(blocks - first, (uint32_t)kSpan<F> / 32);
-    const int pairs = (count + 7) / 8;
-    uint8_t *const scales = &lds.scales[wave][0][0];
-    copy_scales<F, 1>(scales, tiles, end, blocks, first, count, [] {});
-    fix();
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): from here on the compiler can count what is in flight
+    const uint32_t blocks = k / 32, pairs = (blocks + 7) / 8;
     // this thread's part of a piece, of a column of each tile
     const int part = threadIdx.x & 31, c = threadIdx.x >> 5;
     const uint16_t *x[XT];
 #pragma unroll
-    for (int i = 0; i < XT; ++i) x[i] = column(i, c) + start;
+    for (int i = 0; i < XT; ++i) x[i] = column(i, c);
     u32x4 xr[2][XT], p[2][2][2];
-    const auto load_x = [&](u32x4 (&v)[XT], int d) {
-        const bool in = d * 32 + part < (int)count * 4;
+    Bytes16 sc;
+    const auto load_x = [&](u32x4 (&v)[XT], uint32_t d) {
+        const bool in = d * 256 + part * 8 < (uint32_t)k;
 #pragma unroll
         for (int i = 0; i < XT; ++i) {
             v[i] = ld16(x[i] + (in ? d * 256 + part * 8 : 0));
-            if (!in) v[i] = u32x4{0, 0, 0, 0};  // beyond the span
+            if (!in) v[i] = u32x4{0, 0, 0, 0};
         }
+        fix();
     };
     const auto store_x = [&](const u32x4 (&v)[XT], int buf) {
 #pragma unroll
-        for (int i = 0; i < XT; ++i)
-            lds.x[buf][i][part][c ^ (part & 15)] = v[i];
+        for (int i = 0; i < XT; ++i) lds.x[buf][i][part][c ^ (part & 15)] = v[i];
     };
-    const uint32_t row_at = row * blocks + first;
-    const auto load_w = [&](u32x4 (&q)[2][2], uint32_t d) {
+    const auto load_w = [&](u32x4 (&q)[2][2], int turn, uint32_t d) {
+        const Pair t = rows(turn);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                q[h][i] = ld16(tiles[i].w + (row_at + min(8 * d + 4 * h + quarter, count - 1)) * 16);
+                q[h][i] = ld16(t.tile[i].w + (row * blocks + min(8 * d + 4 * h + quarter, blocks - 1)) * 16);
+        fix();
     };
+    static_assert(kScaleTurn == 32, "16 bytes a lane, of 32 rows");
+    const auto load_s = [&](int turn, uint32_t d) {  // for pieces d, d + 1, ... d + EVERY - 1
+        const Pair t = rows(turn);
+        const uint32_t at = d * 8 * EACH + (lane & 1) * 16;
+        sc.load((lane < 32 ? t.tile[0].s : t.tile[1].s) + ((lane / 2 & 15) * blocks * EACH + (at < blocks * EACH ? at : 0)), end);
+        fix();
+    };
+    const auto store_s = [&] { lds.scales[wave][lane / 2][lane & 1] = sc.value(); };
+    uint32_t scale[2][2][2];  // [piece % 2][half][tile]
+    const auto read_s = [&](uint32_t (&v)[2][2], uint32_t d) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *at = reinterpret_cast<const uint8_t *>(lds.scales[wave][i * 16 + row]) +
+                                    (min(8 * d + 4 * h + quarter, blocks - 1) - d / EVERY * EVERY * 8) * EACH;
+                if constexpr (F == MX) v[h][i] = *at;
+                else v[h][i] = *reinterpret_cast<const uint16_t *>(at);
+            }
+    };
+    const auto next = [&](int &turn, uint32_t &d) {  // the piece after, or the same where there is none
+        if (d + 1 < pairs) ++d;
+        else if (turn + 1 < turns) ++turn, d = 0;
+    };
+    int turn = 0, turn_w = 0;
+    uint32_t d = 0, d_w = 0, d_x = 0;
+    int turn_x = 0;
+    load_s(0, 0);
+    load_w(p[0], 0, 0);
     load_x(xr[0], 0);
-    fix();
-    load_x(xr[1], 1);
-    fix();
-    load_w(p[0], 0);
-    fix();
+    next(turn_x, d_x);
+    load_x(xr[1], d_x);
+    next(turn_w, d_w);
+    store_s();
+    read_s(scale[0], 0);
     store_x(xr[0], 0);
     lds_barrier();
-    for (int d0 = 0;; d0 += 2) {
+    f32x4 acc[2][XT] = {};
+    for (;;) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int d = d0 + u;
-            if (d >= pairs) goto done;
-            load_x(xr[u], d + 2);
-            fix();
-            load_w(p[u ^ 1], d + 1);
-            fix();
+            const bool first = d % EVERY == 0;
+            if (first) {  // the next 32 bytes' turn
+                const bool more = d + EVERY < pairs;
+                load_s(more ? turn : min(turn + 1, turns - 1), more ? d + EVERY : 0);
+            }
+            next(turn_x, d_x);
+            load_x(xr[u], d_x);
+            load_w(p[u ^ 1], turn_w, d_w);
+            next(turn_w, d_w);
+            // Groups of steps with four column tiles' operands: a group's come from LDS while the one before is multiplied.
+            constexpr int GROUP = 4 / XT;
+            bf16x8 v[2][GROUP][XT];
+            const auto read_x = [&](int g) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t scale[2];
+                for (int q = 0; q < GROUP; ++q)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    scale[i] = scale_of<F>(scales, i * 16 + row, min(8 * d + 4 * h + quarter, count - 1));
+                    for (int m = 0; m < XT; ++m) {
+                        const int step = g * GROUP + q, at = (step / 4 * 4 + quarter) * 4 + step % 4;
+                        v[g & 1][q][m] = kv::as_bf16x8(lds.x[u][m][at][row ^ (at & 15)]);
+                    }
+            };
+            read_x(0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int at = (h * 4 + quarter) * 4 + j;
-                    bf16x8 v[XT];
+            for (int g = 0; g < 8 / GROUP; ++g) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (g + 1 < 8 / GROUP) read_x(g + 1);
 #pragma unroll
-                    for (int m = 0; m < XT; ++m) v[m] = kv::as_bf16x8(lds.x[u][m][at][row ^ (at & 15)]);
+                for (int q = 0; q < GROUP; ++q) {
+                    const int step = g * GROUP + q;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const bf16x8 e = expand<F>(p[u][h][i][j], scale[i], j);
+                        const bf16x8 e = expand<F>(p[u][step / 4][i][step % 4], scale[u][step / 4][i], step % 4);
 #pragma unroll
                         for (int m = 0; m < XT; ++m)
-                            acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e, v[m], acc[i][m], 0, 0, 0);
+                            acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(e, v[g & 1][q][m], acc[i][m], 0, 0, 0);
                     }
                 }
             }
             fix();
+            if (d % EVERY == EVERY - 1 || d + 1 == pairs) store_s();
+            if (d + 1 == pairs) {
+                done(turn, acc);
+                if (turn + 1 == turns) return;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int m = 0; m < XT; ++m) acc[i][m] = f32x4{0, 0, 0, 0};
+            }
+            next(turn, d);
+            read_s(scale[u ^ 1], d);
             store_x(xr[u ^ 1], u ^ 1);
             lds_barrier();
         }
     }
-done:;
 }
 
 template <int F, int XT>
-__device__ __forceinline__ void gate_up(const Args &a, Shared &lds, int tile, int expert, int n, const int *list) {
+__device__ __forceinline__ void gate_up(const Args &a, Shared &lds, int group, int turns, int expert, int n, const int *list) {
     const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
-    const bool mine = tile < a.inter / 16;
-    const int at = min(tile, a.inter / 16 - 1) * 16;
-    const int64_t first = (int64_t)expert * 2 * a.inter + at;
-    const Tile tiles[2] = {tile_of<F>(a.w13, a.s13, first, a.hidden), tile_of<F>(a.w13, a.s13, first + a.inter, a.hidden)};
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), units = a.inter / 16;
+    const auto rows = [&](int turn) {
+        const int64_t first = (int64_t)expert * 2 * a.inter + min((group + turn) * kWaves + wave, units - 1) * 16;
+        return Pair{{tile_of<F>(a.w13, a.s13, first, a.hidden), tile_of<F>(a.w13, a.s13, first + a.inter, a.hidden)}};
+    };
     const auto column = [&](int m, int c) { return a.x + (int64_t)(list[min(16 * m + c, n - 1)] / a.top) * a.xs; };
-    f32x4 acc[2][XT] = {};
-    const uint8_t *const end = scales_end<F>(a.s13, a, 2 * a.inter, a.hidden);
-    for (int k = 0; k < a.hidden; k += kSpan<F>) stream<F, XT>(lds, tiles, end, column, a.hidden, k, acc);
     const float f = F == NV ? a.f13[expert] : 1.0f;
+    int to[XT];
 #pragma unroll
-    for (int m = 0; m < XT; ++m) {
-        if (!mine || 16 * m + row >= n) continue;
-        uint16_t hi[4], lo[4];
+    for (int m = 0; m < XT; ++m) to[m] = list[min(16 * m + row, n - 1)];
+    const auto done = [&](int turn, const f32x4 (&acc)[2][XT]) {
+        const int unit = (group + turn) * kWaves + wave;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split(silu(acc[0][m][i] * f) * (acc[1][m][i] * f), hi[i], lo[i]);
-        const int64_t to = (int64_t)list[16 * m + row] * a.inter + at + quarter * 4;
-        *reinterpret_cast<u32x2 *>(a.hi + to) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-        *reinterpret_cast<u32x2 *>(a.lo + to) = u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
-    }
+        for (int m = 0; m < XT; ++m) {
+            if (unit >= units || 16 * m + row >= n) continue;
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split(silu(acc[0][m][i] * f) * (acc[1][m][i] * f), hi[i], lo[i]);
+            const int64_t at = (int64_t)to[m] * a.inter + unit * 16 + quarter * 4;
+            *reinterpret_cast<u32x2 *>(a.hi + at) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+            *reinterpret_cast<u32x2 *>(a.lo + at) = u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+        }
+    };
+    stream<F, XT>(lds, turns, rows, scales_end<F>(a.s13, a, 2 * a.inter, a.hidden), column, a.hidden, done);
 }
 
 // The columns are h's upper halves and its rests: eight of each in one tile, or the
 // tiles of the one and then those of the other. Either way their sums are added at the end, so that
 // no result depends on which assignments come together.
 template <int F, int XT>
-__device__ __forceinline__ void down(const Args &a, Shared &lds, int tile, int expert, int n, const int *list) {
+__device__ __forceinline__ void down(const Args &a, Shared &lds, int group, int turns, int expert, int n, const int *list) {
     const int lane = threadIdx.x & 63, row = lane & 15, quarter = lane >> 4;
-    const bool mine = tile < a.hidden / 32;
-    const int at = min(tile, a.hidden / 32 - 1) * 32;
-    const int64_t first = (int64_t)expert * a.hidden + at;
-    const Tile tiles[2] = {tile_of<F>(a.w2, a.s2, first, a.inter), tile_of<F>(a.w2, a.s2, first + 16, a.inter)};
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), units = a.hidden / 32;
+    const auto rows = [&](int turn) {
+        const int64_t first = (int64_t)expert * a.hidden + min((group + turn) * kWaves + wave, units - 1) * 32;
+        return Pair{{tile_of<F>(a.w2, a.s2, first, a.inter), tile_of<F>(a.w2, a.s2, first + 16, a.inter)}};
+    };
     const auto column = [&](int m, int c) {
         const int at = 16 * m + c, half = 8 * XT;
         return (at < half ? a.hi : a.lo) + (int64_t)list[min(at % half, n - 1)] * a.inter;
@@ -604,63 +670,76 @@ __device__ __forceinline__ void down(const Args &a, Shared &lds, int tile, int e
         to[m] = list[min(16 * m + row, n - 1)];
         weight[m] = a.weights[to[m]] * (F == NV ? a.f2[expert] : 1.0f);
     }
-    f32x4 acc[2][XT] = {};
-    const uint8_t *const end = scales_end<F>(a.s2, a, a.hidden, a.inter);
-    for (int k = 0; k < a.inter; k += kSpan<F>) stream<F, XT>(lds, tiles, end, column, a.inter, k, acc);
+    const auto done = [&](int turn, const f32x4 (&acc)[2][XT]) {
+        const int unit = (group + turn) * kWaves + wave;
 #pragma unroll
-    for (int m = 0; m < OUT; ++m) {
+        for (int m = 0; m < OUT; ++m) {
+            f32x4 v[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                acc[i][m][r] += XT > 1 ? acc[i][(m + OUT) % XT][r] : dpp_f32<0x128>(acc[i][m][r]);  // row_ror:8
-        if (!mine || 16 * m + row >= n || (XT == 1 && row >= 8)) continue;
+                for (int r = 0; r < 4; ++r)
+                    v[i][r] = acc[i][m][r] + (XT > 1 ? acc[i][(m + OUT) % XT][r] : dpp_f32<0x128>(acc[i][m][r]));  // row_ror:8
+            if (unit >= units || 16 * m + row >= n || (XT == 1 && row >= 8)) continue;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<f32x4 *>(a.y + (int64_t)to[m] * a.hidden + at + i * 16 + quarter * 4) = acc[i][m] * weight[m];
-    }
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<f32x4 *>(a.y + (int64_t)to[m] * a.hidden + unit * 32 + i * 16 + quarter * 4) =
+                    v[i] * weight[m];
+        }
+    };
+    stream<F, XT>(lds, turns, rows, scales_end<F>(a.s2, a, a.hidden, a.inter), column, a.inter, done);
 }
 
 template <int F, bool DOWN>
-__global__ __launch_bounds__(kWaves * 64) void k_stream(Args a) {
+__global__ __launch_bounds__(kWaves * 64) void k_stream(Args a, int turns) {
     __shared__ Shared lds;
     const int4 slot = a.slots[blockIdx.y];
-    const int expert = slot.x;
+    const int expert = slot.x, group = blockIdx.x * turns;
     if (expert < 0) return;
-    const int tile = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    turns = min(turns, (a.inter / 16 * !DOWN + a.hidden / 32 * DOWN + kWaves - 1) / kWaves - group);
     const int *list = a.list + slot.y;
     int n = slot.z;
     constexpr int EACH = DOWN ? 8 : 16;  // assignments that a tile of columns holds
-    for (; n > 0; n -= EACH * kTiles, list += EACH * kTiles) {
+    for (;;) {
         const int now = min(n, EACH * kTiles);
         if constexpr (DOWN) {
-            if (now <= EACH) down<F, 1>(a, lds, tile, expert, now, list);
-            else if (now <= 2 * EACH) down<F, 2>(a, lds, tile, expert, now, list);
-            else down<F, 4>(a, lds, tile, expert, now, list);
+            if (now <= EACH) down<F, 1>(a, lds, group, turns, expert, now, list);
+            else if (now <= 2 * EACH) down<F, 2>(a, lds, group, turns, expert, now, list);
+            else down<F, 4>(a, lds, group, turns, expert, now, list);
         } else {
-            if (now <= EACH) gate_up<F, 1>(a, lds, tile, expert, now, list);
-            else if (now <= 2 * EACH) gate_up<F, 2>(a, lds, tile, expert, now, list);
-            else gate_up<F, 4>(a, lds, tile, expert, now, list);
+            if (now <= EACH) gate_up<F, 1>(a, lds, group, turns, expert, now, list);
+            else if (now <= 2 * EACH) gate_up<F, 2>(a, lds, group, turns, expert, now, list);
+            else gate_up<F, 4>(a, lds, group, turns, expert, now, list);
         }
+        n -= EACH * kTiles, list += EACH * kTiles;
+        if (n <= 0) return;
+        lds_barrier();
     }
 }
 
 // out = the sum of a token's weighted results, in the order of its experts.
 __global__ __launch_bounds__(256) void k_add(Args a) {
     const int64_t pieces = (int64_t)a.tokens * (a.hidden / 8);
-    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < pieces; p += (int64_t)gridDim.x * 256) {
-        const int t = (int)(p / (a.hidden / 8)), i = (int)(p - (int64_t)t * (a.hidden / 8)) * 8;
-        float v[8] = {};
-        for (int j = 0; j < a.top; ++j) {
-            const int at = t * a.top + j;
-            if ((uint32_t)a.ids[at] >= (uint32_t)a.experts) continue;
-            const float *y = a.y + (int64_t)at * a.hidden + i;
+    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (p >= pieces) return;
+    const int t = (int)(p / (a.hidden / 8)), i = (int)(p - (int64_t)t * (a.hidden / 8)) * 8;
+    f32x4 sum[2] = {};
+    for (int j0 = 0; j0 < a.top; j0 += 4) {  // four at a time: one after another they are latency alone
+        f32x4 y[4][2];
+        bool in[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] += y[q];
+        for (int j = 0; j < 4; ++j) {
+            const int at = t * a.top + min(j0 + j, a.top - 1);
+            in[j] = j0 + j < a.top && (uint32_t)a.ids[at] < (uint32_t)a.experts;
+            const f32x4 *from = reinterpret_cast<const f32x4 *>(a.y + (int64_t)at * a.hidden + i);
+            y[j][0] = from[0], y[j][1] = from[1];
         }
-        *reinterpret_cast<u32x4 *>(a.out + t * a.os + i) =
-            u32x4{kv::pack2(v[0], v[1]), kv::pack2(v[2], v[3]), kv::pack2(v[4], v[5]), kv::pack2(v[6], v[7])};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (in[j]) sum[0] += y[j][0], sum[1] += y[j][1];
     }
+    *reinterpret_cast<u32x4 *>(a.out + t * a.os + i) = u32x4{kv::pack2(sum[0].x, sum[0].y), kv::pack2(sum[0].z, sum[0].w),
+                                                             kv::pack2(sum[1].x, sum[1].y), kv::pack2(sum[1].z, sum[1].w)};
 }
 
 // Many assignments: lists by expert, and the experts that have any (then -1). One
@@ -714,6 +793,12 @@ Layout layout_of(const qbn_moe_weights &e, int64_t tokens, int top) {
     return l;
 }
 
+// Workgroups that a kernel of streams should have at least, two for a compute unit, before each takes more than one
+// group of rows: with 256 unequal ones the last are waited for (256 columns' worth of 64 experts: 53 and 47 us),
+// with as many as there are, each pays its start (256 tokens of 128 experts, second product: 135 and 127 us).
+constexpr int kEnough = 512;
+
+
 template <int F>
 hipError_t launch(const Args &a, bool few, int32_t *list, int4 *where, hipStream_t s) {
     if (few) {
@@ -724,8 +809,14 @@ hipError_t launch(const Args &a, bool few, int32_t *list, int4 *where, hipStream
     } else {
         const int slots = a.n < a.experts ? a.n : a.experts;
         k_lists<<<1, kListThreads, 0, s>>>(a, list, where);
-        k_stream<F, false><<<dim3((a.inter / 16 + kWaves - 1) / kWaves, slots), kWaves * 64, 0, s>>>(a);
-        k_stream<F, true><<<dim3((a.hidden / 32 + kWaves - 1) / kWaves, slots), kWaves * 64, 0, s>>>(a);
+        const auto turns_of = [&](int groups) {
+            const int t = std::max(1, std::min(groups, groups * slots / kEnough)), n = (groups + t - 1) / t;
+            return (groups + n - 1) / n;
+        };
+        const int up = (a.inter / 16 + kWaves - 1) / kWaves, out = (a.hidden / 32 + kWaves - 1) / kWaves;
+        const int tu = turns_of(up), td = turns_of(out);
+        k_stream<F, false><<<dim3((up + tu - 1) / tu, slots), kWaves * 64, 0, s>>>(a, tu);
+        k_stream<F, true><<<dim3((out + td - 1) / td, slots), kWaves * 64, 0, s>>>(a, td);
         const int64_t blocks = ((int64_t)a.tokens * (a.hidden / 8) + 255) / 256;
         k_add<<<(unsigned)blocks, 256, 0, s>>>(a);
     }
