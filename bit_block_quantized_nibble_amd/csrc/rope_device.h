@@ -24,20 +24,26 @@ __device__ __forceinline__ uint32_t angle_of(int p, u32x2 turns) {
 
 // factor * cos and factor * sin of an angle in 2^-32 turns. The nearest quarter turn
 // is taken off exactly, what is left lies in [-pi/4, pi/4], where the Taylor series
-// to a^9 and a^10 are off by 2e-9 and 1e-10: below half a unit of binary32.
+// to a^9 and a^10 are off by 2e-9 and 1e-10: below half a unit of binary32. What a binary32
+// angle lacks goes into the terms before the last sum, so that a turned number's rounding to
+// fewer bits is hardly ever another one: sines are 0.19 units of 2^-24 off in the mean square (0.33
+// without), where correctly rounded ones are 0.19, cosines 0.31 (0.35), and 0.29.
 __device__ __forceinline__ void cos_sin(uint32_t angle, float factor, float &c, float &s) {
     const uint32_t quarter = (angle + 0x20000000u) >> 30;
-    const float a = (float)(int)(angle - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
-    const float q = a * a;
+    const int left = (int)(angle - (quarter << 30));
+    const float f = (float)left, unit = 1.4629180792671596e-9f;  // 2 pi / 2^32, less the next line's rest
+    const float a = f * unit, q = a * a;
+    float rest = __builtin_fmaf(f, -4.070940267922164e-17f, __builtin_fmaf(f, unit, -a));
+    rest = __builtin_fmaf((float)(left - (int)f), unit, rest);  // what a lacks
     float sn = __builtin_fmaf(q, 2.7557319223985893e-6f, -1.984126984126984e-4f);
     sn = __builtin_fmaf(q, sn, 8.333333333333333e-3f);
     sn = __builtin_fmaf(q, sn, -1.6666666666666666e-1f);
-    sn = __builtin_fmaf(q * a, sn, a);
+    sn = a + __builtin_fmaf(q * a, sn, rest * __builtin_fmaf(q, -0.5f, 1.0f));
     float cs = __builtin_fmaf(q, -2.755731922398589e-7f, 2.48015873015873e-5f);
     cs = __builtin_fmaf(q, cs, -1.388888888888889e-3f);
     cs = __builtin_fmaf(q, cs, 4.1666666666666664e-2f);
     cs = __builtin_fmaf(q, cs, -0.5f);
-    cs = __builtin_fmaf(q, cs, 1.0f);
+    cs = 1.0f + __builtin_fmaf(q, cs, -(rest * a));
     const bool swap = quarter & 1u;
     c = (swap ? sn : cs) * factor;
     s = (swap ? cs : sn) * factor;
