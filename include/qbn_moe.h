@@ -14,8 +14,8 @@
  * binary64 (the products are exact). The top_k largest of each token are its
  * experts, in falling order, equal ones by their number. Their weights are the
  * softmax over the chosen logits (normalize != 0) or over all experts'
- * (normalize == 0), in binary64, rounded to binary32. NaN ranks below every
- * number, and a token with a logit of NaN or +inf, or with none above -inf,
+ * (normalize == 0), in binary64, rounded to binary32. NaN ranks as -inf
+ * does, below every finite number, and a token with a logit of NaN or +inf, or with none above -inf,
  * has weights of NaN; ids are valid and distinct in any case.
  *
  * The experts. For token t with experts e_j and weights w_j:
@@ -26,8 +26,8 @@
  * weight. A token without experts gives 0. The same expert twice counts twice.
  * Weights enter the products as bfloat16, which holds every E2M1 value times
  * its scale exactly but for MXFP4 scale bytes from 253 on (which may pass its
- * largest) and 0 with code 1 or 9 (kept, as a subnormal); products are exact
- * and sums binary32. h is held as the sum of two bfloat16 values (2^-16
+ * largest: infinity, and NaN where a product of it is 0 or they cancel) and 0
+ * with code 1 or 9 (kept, as a subnormal); products are exact and sums binary32. h is held as the sum of two bfloat16 values (2^-16
  * relative). NVFP4's factor per expert is applied to the sums.
  */
 #ifndef QBN_MOE_H
