@@ -10,6 +10,9 @@
 // elements a lane, as the blocks of the MX formats want them (four lanes a block of 32),
 // with the eight that they are paired with read beside them (from the same lines);
 // queries go by eight pairs a lane, which lets them be turned in their place.
+//
+// 32 sequences' one token, 32 and 8 heads of 128, MXFP8: 4.8 us, a chain of dependent loads (length,
+// page, elements) and a launch. 4789 tokens of four prompts: 25 us, 4.4 TB/s; bound by HBM.
 #include "kv_store.h"
 #include "rope_device.h"
 #include "rope_launch.h"

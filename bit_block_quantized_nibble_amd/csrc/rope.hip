@@ -3,12 +3,15 @@
 //   a' = f (a cos t - b sin t),  b' = f (b cos t + a sin t)
 // for pairs (a, b) of the first `rot` elements of a head, t = position *
 // frequency. Bound by latency for a step's few tokens and by HBM for prompts: each
-// element is read and written once. Cosine and sine are computed, 22 instructions a
+// element is read and written once. Cosine and sine are computed, 29 instructions a
 // pair, once for all heads of a token: a lane has the same 16 elements (eight
 // pairs) of every head that it comes to, a wave 64 / (dim / 16) heads at a time. With
 // tables of cosines instead a token would read another 4 bytes an element of one head,
 // at positions that are not known in advance. Where tokens are few a token's heads are
 // spread over waves, each with angles of its own.
+//
+// 16384 tokens of 40 heads of 128, bf16: 67 us, 5.0 TB/s, a large copy's rate; 16 tokens: 3.3 us,
+// of which 2.4 are an empty kernel's.
 #include "rope_device.h"
 #include "rope_launch.h"
 

@@ -28,6 +28,7 @@ def check(rng, fmt, tokens, experts, top, hidden, inter, ids=None):
     (1, 2048, 32), (3, 2080, 64), (2, 4096, 32), (1, 4128, 4128), (7, 4160, 96), (2, 8224, 32),
     (8, 16416, 32),  # LDS holds three of the tokens at a time
     (1, 32, 16416), (8, 64, 8224),  # h does not fit LDS
+    (1, 65024, 32), (1, 32, 16128),  # as much as fits
     (2, 65536, 32),  # nor one token
     (9, 4128, 160), (20, 2080, 4128)])
 def test_long_rows(fmt, tokens, hidden, inter):
