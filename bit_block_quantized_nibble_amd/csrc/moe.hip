@@ -212,42 +212,37 @@ __device__ __forceinline__ void stage(uint8_t *lds, int rows, int k, const From 
     }
 }
 
-// COUNT pairs of steps from `first`, `every` apart, of NT tiles. In pairs, since a
+// COUNT pairs of steps from `first`, `every` apart, of a row tile. In pairs, since a
 // row's two 64-byte halves of a line go through the first cache together then.
-template <int F, int NT, int COUNT>
+template <int F, int COUNT>
 struct Batch {
-    u32x4 codes[COUNT][2][NT];
-    uint32_t scale[COUNT][2][NT];
+    u32x4 codes[COUNT][2];
+    uint32_t scale[COUNT][2];
 
-    __device__ __forceinline__ void load(const Tile (&tiles)[NT], uint32_t blocks, uint32_t first, uint32_t every) {
+    __device__ __forceinline__ void load(const Tile &tile, uint32_t blocks, uint32_t first, uint32_t every) {
         const uint32_t lane = threadIdx.x & 63, row = (lane & 15) * blocks;
 #pragma unroll
         for (int u = 0; u < COUNT; ++u)
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {  // beyond the row: its last block, and x is 0 there or not looked at
-                    const uint32_t at = row + min(8 * (first + u * every) + 4 * h + (lane >> 4), blocks - 1);
-                    codes[u][h][i] = ld16(tiles[i].w + at * 16);
-                    if constexpr (F == MX) scale[u][h][i] = tiles[i].s[at];
-                    else scale[u][h][i] = *reinterpret_cast<const uint16_t *>(tiles[i].s + 2 * at);
-                }
+            for (int h = 0; h < 2; ++h) {  // beyond the row: its last block, and h is 0 there or not looked at
+                const uint32_t at = row + min(8 * (first + u * every) + 4 * h + (lane >> 4), blocks - 1);
+                codes[u][h] = ld16(tile.w + at * 16);
+                if constexpr (F == MX) scale[u][h] = tile.s[at];
+                else scale[u][h] = *reinterpret_cast<const uint16_t *>(tile.s + 2 * at);
+            }
     }
     // Pairs below `pairs`. x: this lane's column in LDS, at its quarter
-    __device__ __forceinline__ void multiply(const uint8_t *x, int pairs, int first, int every, f32x4 (&acc)[NT]) const {
+    __device__ __forceinline__ void multiply(const uint8_t *x, int pairs, int first, int every, f32x4 &acc) const {
 #pragma unroll
         for (int u = 0; u < COUNT; ++u) {
             const int d = first + u * every;
-            if (COUNT > 1 && d >= pairs) break;
+            if (d >= pairs) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bf16x8 v = kv::as_bf16x8(ld16(x + d * 512 + h * 256 + 16 * j));
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand<F>(codes[u][h][i][j], scale[u][h][i], j), v,
-                                                                         acc[i], 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(expand<F>(codes[u][h][j], scale[u][h], j), v, acc, 0, 0, 0);
                 }
         }
     }
@@ -329,6 +324,8 @@ __global__ __launch_bounds__(kGateWaves * 64, 3) void k_gate_up_few(Args a, int 
                         [&](int c) { return a.x + (int64_t)(nth_bit(m, g + c) / a.top) * a.xs; }, then);
                 else then();
             };
+            // Half of the loads where half are enough: the others would ask for the last block again (rows of 2048:
+            // 9.9 us, else 11.6).
             constexpr int kMost = kSpan<F> / 256 / kGateWaves;
             if (here <= 16 * kGateWaves / 2 * (kMost / 2))
                 gate_up_span<F, kMost / 2>(scales, tiles, end, blocks, start, here, x, stage_x, acc);
@@ -383,9 +380,9 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down_few(Args a) {
     struct Item {
         uint64_t m;  // its assignments
         int p;       // its part: pairs p, p + parts, ...
-        Tile tiles[1];
+        Tile tile;
         u32x4 h[kDownBatch];  // of the first assignment
-        Batch<F, 1, kDownBatch> batch;
+        Batch<F, kDownBatch> batch;
     };
     // Pairs t, t + parts, ... of an assignment's h: lanes 0 .. 31 the upper halves, the others the rests.
     const auto load_h = [&](u32x4 (&h)[kDownBatch], int at, int t) {
@@ -407,9 +404,9 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down_few(Args a) {
         int expert;
         it.m = same_expert(id, valid, nth_bit(leaders, item % found), expert);
         it.p = item / found;
-        it.tiles[0] = tile_of<F>(a.w2, a.s2, (int64_t)expert * a.hidden + blockIdx.x * 16, a.inter);
+        it.tile = tile_of<F>(a.w2, a.s2, (int64_t)expert * a.hidden + blockIdx.x * 16, a.inter);
         load_h(it.h, nth_bit(it.m, 0), it.p);
-        it.batch.load(it.tiles, blocks, it.p, parts);
+        it.batch.load(it.tile, blocks, it.p, parts);
         fix();
     };
     Item it;
@@ -422,9 +419,9 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down_few(Args a) {
         for (int g = 0; g < n; g += 8) {
             const int at = nth_bit(it.m, min(g + (row & 7), n - 1));
             const uint8_t *x = hs + (2 * at + (row >> 3)) * pitch + quarter * 64;
-            f32x4 acc[1] = {};
+            f32x4 acc = {};
             for (int t = it.p; t < pairs; t += parts * kDownBatch) {
-                if (t != it.p || g) it.batch.load(it.tiles, blocks, t, parts);
+                if (t != it.p || g) it.batch.load(it.tile, blocks, t, parts);
                 if (g == 0)
                     for (int c = 0; c < n; ++c) {
                         if (t != it.p || c) load_h(it.h, nth_bit(it.m, c), t);
@@ -433,7 +430,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_down_few(Args a) {
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 it.batch.multiply(x, pairs, t, parts, acc);
             }
-            f32x4 v = acc[0];
+            f32x4 v = acc;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += dpp_f32<0x128>(v[i]);  // row_ror:8: the rest's column
             if (row < 8 && g + row < n) *reinterpret_cast<f32x4 *>(&part[it.p * a.n + at][quarter * 4]) = v;
@@ -776,7 +773,8 @@ __global__ __launch_bounds__(kListThreads) void k_lists(Args a, int32_t *list, i
     }
 }
 
-// The form for few tokens, where x and h fit LDS.
+// The form for few tokens, where x and h fit LDS: both products of one token (8 of 64 experts, 4096 x 1536) take 23 us, 43
+// in the other form with its lists and sums; of 7 tokens (4 of 32, 1120 x 736, nvfp4) 22 and 31.
 constexpr int kFewLds = 128 << 10;
 bool is_few(const qbn_moe_weights &e, int64_t tokens, int top) {
     return tokens <= kFewTokens && tokens * top <= kFew && few_pitch(e.hidden) <= kFewLds &&
