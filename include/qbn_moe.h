@@ -71,7 +71,9 @@ QBN_API size_t qbn_moe_struct_size(int32_t which);
  * experts each: for the choice (experts NULL), for the experts' products
  * (router NULL), or for both; -1 where an argument is not valid. Device,
  * 16-byte aligned, any content; not kept: calls that follow each other on a
- * stream may share it. */
+ * stream may share it, and one that serves a number of tokens serves every
+ * smaller one. What a call writes (ids, weights, out, the workspace) shares
+ * no byte with anything else that it is given. */
 QBN_API int64_t qbn_moe_workspace(const qbn_moe_router *router, const qbn_moe_weights *experts, int64_t tokens,
                                   int32_t top_k);
 
