@@ -40,6 +40,8 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {  // rotation, dev
         const int32_t *pos = ints(tensor(a[3], "positions"), tokens, dev, "positions", kOwner);
         at::Tensor out = vectors_out(a[4], t, t.scalar_type(), dtype == QBN_F32 ? "torch.float32" : "torch.bfloat16", dev, kOwner);
         const Rows o = vectors(out, 0, dim, dev, "out", kOwner);
+        // A rotation made on the host is on the same "device" as host tensors: their addresses are no kernel's.
+        if (dev < 0) refuse(PyExc_ValueError, "x and the rotation must be on a device (cuda); x is on %s", words(t).c_str());
         const auto small = [](int64_t v) { return v > INT32_MAX ? -1 : (int32_t)v; };  // refused, not wrapped
         const int32_t st = qbn_rope(r, tokens, small(heads), small(dim), pos, t.data_ptr(), x.token, x.head, out.data_ptr(),
                                     o.token, o.head, dtype, OnDevice(dev));

@@ -104,7 +104,8 @@ class Rope:
     """A rotation by positions: `frequencies` (radians per position, one for each
     of the rot / 2 pairs, any sequence of numbers; taken in binary64), the layout
     of the pairs ("half": element i with i + rot / 2, "interleaved": 2 i with
-    2 i + 1) and the factor on cosine and sine."""
+    2 i + 1) and the factor on cosine and sine. One made on the host (device "cpu")
+    holds its turns there and turns nothing: rope and kv_append_rope refuse it."""
 
     turns = _fixed("turns", "Turns per position of each pair, in units of 2^-64 (int64 of the same bits).")
 
