@@ -66,7 +66,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", sca
             p f_i + (1 - p) f_i / scale with p = (n - low) / (high - low).
     yarn    the same with p = 1 - clamp((i - a) / (b - a)), where a and b are the
             pairs (rounded outwards, in 0 .. rot - 1) that make `fast` and `slow`
-            turns; the factor is 0.1 ln scale + 1.
+            turns; the factor is 0.1 ln scale + 1, and 1 where scale is no more than 1.
     """
     if rot < 2 or rot % 2:
         raise ValueError("rot must be a positive even number")
@@ -96,7 +96,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", sca
         a, b = max(0, math.floor(a)), min(rot - 1, math.ceil(b))
         part = [min(1.0, max(0.0, (i - a) / max(b - a, 0.001))) for i in range(rot // 2)]
         f = [x * (1 - p) + x / scale * p for x, p in zip(f, part)]
-        factor = 0.1 * math.log(scale) + 1.0
+        factor = 0.1 * math.log(scale) + 1.0 if scale > 1 else 1.0
     return f, factor
 
 
