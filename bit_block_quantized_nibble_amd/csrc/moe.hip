@@ -847,11 +847,11 @@ hipError_t launch_moe_experts(const qbn_moe_weights &e, int64_t tokens, int top_
     int32_t *list = (int32_t *)(b + l.list);
     int4 *slots = (int4 *)(b + l.slots);
     a.list = list, a.slots = slots;
+    const bool few = is_few(e, tokens, top_k);  // of the whole call: the last portion's tokens are summed as the others'
     for (int64_t at = 0; at < tokens; at += QBN_MOE_PORTION) {
         a.tokens = (int)(tokens - at < QBN_MOE_PORTION ? tokens - at : QBN_MOE_PORTION), a.n = a.tokens * top_k;
         a.x = (const uint16_t *)x + at * x_stride, a.out = (uint16_t *)out + at * out_stride;
         a.ids = ids + at * top_k, a.weights = weights + at * top_k;
-        const bool few = is_few(e, a.tokens, top_k);
         const hipError_t st = e.format == QBN_MXFP4 ? launch<MX>(a, few, list, slots, s) : launch<NV>(a, few, list, slots, s);
         if (st != hipSuccess) return st;
     }
