@@ -223,10 +223,13 @@ hipError_t launch_moe_route(const qbn_moe_router &r, int64_t tokens, const void 
     Args a = {};
     a.w = (const __bf16 *)r.weight, a.bias = r.bias, a.logits = (double *)ws, a.xs = x_stride;
     a.experts = r.experts, a.hidden = r.hidden, a.top = r.top_k, a.normalize = r.normalize;
+    // Form and parts are the whole call's: the last portion's logits are summed in the same order as the others'.
+    const bool few = tokens <= kFew;
+    a.parts = parts_of(r, tokens);
     for (int64_t at = 0; at < tokens; at += kPortion) {
-        a.tokens = (int)std::min(tokens - at, kPortion), a.parts = parts_of(r, a.tokens);
+        a.tokens = (int)std::min(tokens - at, kPortion);
         a.x = (const __bf16 *)x + at * x_stride, a.ids = ids + at * r.top_k, a.weights = weights + at * r.top_k;
-        if (a.tokens <= kFew) {
+        if (few) {
             (a.tokens == 1 ? k_logits_few<1> : k_logits_few<2>)<<<r.experts, 256, 0, s>>>(a);
         } else {
             const int tiles = (a.tokens + 15) / 16 * ((a.experts + 15) / 16);
