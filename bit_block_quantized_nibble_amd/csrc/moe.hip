@@ -13,8 +13,8 @@
 // they have the same 8 elements each in one 16-byte load of x.
 //
 // First kernel: h for each assignment, from 16 gate rows and the 16 up rows beside them.
-// h goes on as two bfloat16 values, the upper bits and the rest: one alone would round it
-// by 2^-9, as much as the output's own rounding. Second kernel: the same products with
+// h goes on as two bfloat16 values, the nearest one and the rest: one alone would round it
+// by 2^-8, as much as the output's own rounding. Second kernel: the same products with
 // W2. Where tokens are few, a workgroup has 16 output rows of all of them and adds up the
 // tokens' experts itself; else the assignments' results go to memory and one more kernel
 // adds them, in the order of a token's choices: the same bits every time.
@@ -43,7 +43,7 @@ struct Args {
     const float *weights;
     uint16_t *out;
     int64_t xs, os;
-    uint16_t *hi, *lo;  // h [assignments][inter], upper bits and rest
+    uint16_t *hi, *lo;  // h [assignments][inter], its bfloat16 and the rest
     float *y;           // [assignments][hidden]: results of W2, weighted (many assignments)
     const int32_t *list;  // more tokens: assignments by expert
     const int4 *slots;    // and each expert that has any: {its number, where its list begins, how many}; then {-1}
@@ -84,16 +84,19 @@ __device__ __forceinline__ bf16x8 expand(uint32_t c, uint32_t scale, int i) {
     return kv::as_bf16x8(o);
 }
 
-// The upper bits of h, and what they leave out, both bfloat16. Cut, not rounded: the
-// upper part then is no infinity where h is none.
+// h rounded to bfloat16, and what that leaves out, bfloat16 too: at most half of the first's
+// last bit, 2^-8 of it, so that its own rounding is off by 2^-17 of h at most (with the first
+// cut instead, 2^-16: twice as many outputs were rounded to another number than the nearest).
+// Only where rounding would pass the largest number the first is cut: a finite h stays so.
 __device__ __forceinline__ void split(float h, uint16_t &hi, uint16_t &lo) {
     const uint32_t b = __float_as_uint(h);
     if ((b & 0x7F800000u) == 0x7F800000u) {
         hi = bf16_bits_rne(h);
         lo = 0;
     } else {
-        hi = (uint16_t)(b >> 16);
-        lo = bf16_bits_rne(h - __uint_as_float(b & 0xFFFF0000u));
+        const uint16_t near = bf16_bits_rne(h);
+        hi = (near & 0x7F80u) == 0x7F80u ? (uint16_t)(b >> 16) : near;
+        lo = bf16_bits_rne(h - __uint_as_float((uint32_t)hi << 16));
     }
 }
 

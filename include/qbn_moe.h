@@ -27,7 +27,7 @@
  * Weights enter the products as bfloat16, which holds every E2M1 value times
  * its scale exactly but for MXFP4 scale bytes from 253 on (which may pass its
  * largest: infinity, and NaN where a product of it is 0 or they cancel) and 0
- * with code 1 or 9 (kept, as a subnormal); products are exact and sums binary32. h is held as the sum of two bfloat16 values (2^-16
+ * with code 1 or 9 (kept, as a subnormal); products are exact and sums binary32. h is held as the sum of two bfloat16 values (2^-17
  * relative). NVFP4's factor per expert is applied to the sums.
  */
 #ifndef QBN_MOE_H
