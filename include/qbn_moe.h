@@ -25,10 +25,13 @@
  * An id that is no expert's stands for none: it adds nothing, whatever its
  * weight. A token without experts gives 0. The same expert twice counts twice.
  * Weights enter the products as bfloat16, which holds every E2M1 value times
- * its scale exactly but for MXFP4 scale bytes from 253 on (which may pass its
- * largest: infinity, and NaN where a product of it is 0 or they cancel) and 0
- * with code 1 or 9 (kept, as a subnormal); products are exact and sums binary32. h is held as the sum of two bfloat16 values (2^-17
- * relative). NVFP4's factor per expert is applied to the sums.
+ * its scale exactly (scale byte 0 with code 1 or 9 as a subnormal) but for
+ * those that pass its largest, with MXFP4 scale bytes 253 and 254: they are
+ * infinite, and every sum that one enters is infinite or NaN. (Of the products
+ * of such a block some may be with zeros that pad x or h, or with a part of h
+ * that is 0.) Products are exact and sums binary32. h is held as the sum of two
+ * bfloat16 values (2^-17 relative). NVFP4's factor per expert is applied to the
+ * sums.
  */
 #ifndef QBN_MOE_H
 #define QBN_MOE_H
