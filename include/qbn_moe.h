@@ -30,7 +30,8 @@
  * infinite, and every sum that one enters is infinite or NaN. (Of the products
  * of such a block some may be with zeros that pad x or h, or with a part of h
  * that is 0.) Products are exact and sums binary32. h is held as the sum of two
- * bfloat16 values (2^-17 relative). NVFP4's factor per expert is applied to the
+ * bfloat16 values (2^-17 relative), and silu(a) for a < -87 may be 0 instead of
+ * less than 2^-119. NVFP4's factor per expert is applied to the
  * sums.
  */
 #ifndef QBN_MOE_H
