@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import math
-from fractions import Fraction
 from typing import Optional, Sequence, Union
 
 import torch
@@ -20,7 +19,8 @@ from .kv import KVCache, _fixed
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_EXPORTED = ("qbn_rotation_struct_size", "qbn_rope", "qbn_kv_append_rope")
-_PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+_TWO_PI = 628318530717958647692528676655900576839433879875021164194988918  # 10^62 of it
+_ONE = 10 ** 62 << 64
 
 
 class _CRotation(ctypes.Structure):
@@ -100,6 +100,14 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", sca
     return f, factor
 
 
+def _turns(frequency: float) -> int:
+    """The frequency in whole turns of 2^64 parts, to the nearest part (ties, which an
+    irrational number's multiples do not have, aside), as the int64 of the same bits."""
+    n, d = frequency.as_integer_ratio()
+    d *= _TWO_PI
+    return ((2 * n * _ONE + d) // (2 * d) + (1 << 63) & (1 << 64) - 1) - (1 << 63)
+
+
 class Rope:
     """A rotation by positions: `frequencies` (radians per position, one for each
     of the rot / 2 pairs, any sequence of numbers; taken in binary64), the layout
@@ -120,8 +128,7 @@ class Rope:
             raise ValueError("%d frequencies: a positive multiple of 8 is wanted (rot a multiple of 16)" % len(f))
         if not all(math.isfinite(x) for x in f) or not math.isfinite(factor):
             raise ValueError("frequencies and factor must be finite")
-        turns = [round(Fraction(x) / (2 * _PI) * (1 << 64)) % (1 << 64) for x in f]
-        self._turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self._turns = torch.tensor([_turns(x) for x in f], dtype=torch.int64, device=device)
         self.layout, self.rot, self.factor, self.frequencies = layout, 2 * len(f), float(factor), f
         self.index = self._turns.get_device() if self._turns.is_cuda else -1
         _rope_lib()
