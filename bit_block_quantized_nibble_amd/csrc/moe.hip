@@ -2,7 +2,8 @@
 //
 //   out_t = sum_j w_tj W2[e] (silu(Wg[e] x_t) * (Wu[e] x_t)),  e = ids[t][j]
 // An assignment a = t * top_k + j is a token's j-th expert. Bound by the weights'
-// bytes: each of a layer's active experts is read once, for one token or for sixty-four.
+// bytes: each of a layer's active experts is read once for up to 64 of its assignments in the first
+// product and 32 in the second, and again for more, and for each 256 tokens.
 // So the weights go from memory to registers with nothing in between, are expanded
 // there to bfloat16 (exactly) and multiplied on the matrix cores with the tokens as
 // columns, 16 of them at the price of one.
@@ -21,8 +22,9 @@
 //
 // One token, 8 of 64 experts, 4096 x 1536, MXFP4: 13.5 and 9.2 us for 53 and 27 MB, bound by chains
 // of dependent loads (of the first kernel's, 8 are the codes' way). 256 tokens, 8 of 128 such experts: 178 us
-// for 856 MB, 4.8 TB/s, a large copy's rate and what its loads take alone; 127 for 428 MB, whose
-// columns, two halves of h, are as many bytes again from the second cache and through LDS.
+// for 856 MB, 4.8 TB/s, a large copy's rate and what its loads take alone; 127 for 428 MB, beside which
+// the columns, two parts of h, are another 201 MB for its 16 groups of rows (5.4 million line requests in
+// all, of which 3.1 are codes; a request in nine is met by the second cache), all through LDS.
 #include "kv_device.h"
 #include "moe_launch.h"
 
@@ -776,8 +778,11 @@ __global__ __launch_bounds__(kListThreads) void k_lists(Args a, int32_t *list, i
     }
 }
 
-// The form for few tokens, where x and h fit LDS: both products of one token (8 of 64 experts, 4096 x 1536) take 23 us, 43
-// in the other form with its lists and sums; of 7 tokens (4 of 32, 1120 x 736, nvfp4) 22 and 31.
+// The form for few tokens, where x and h fit LDS: both products of one token (8 of 64 experts, 4096 x 1536) take 23 us, 44
+// in the other form with its lists and sums; of two (96 KiB of h) 39 and 47; of 7 tokens (4 of 32, 1120 x 736, nvfp4) 22 and
+// 29; of one (2 of 8, 4096 x 14336, 112 KiB) 52 and 107. The bound on h lies below what the kernel's own 8.5 KiB leave of a
+// workgroup's 160, and short of where the forms cross: from 128 KiB on this one would be ahead by 2 % (two tokens, inter
+// 2048, 128.5 KiB: 51.8 and 52.7) to a fifth (three, inter 1536, 145 KiB: 50 and 65).
 constexpr int kFewLds = 128 << 10;
 bool is_few(const qbn_moe_weights &e, int64_t tokens, int top) {
     return tokens <= kFewTokens && tokens * top <= kFew && few_pitch(e.hidden) <= kFewLds &&
@@ -802,9 +807,10 @@ Layout layout_of(const qbn_moe_weights &e, int64_t tokens, int top) {
 
 // Workgroups that a kernel of streams should have at least, two for a compute unit, before each takes more than one
 // group of rows: with 256 the last are waited for (64 tokens of 64 experts, first product: 53 us, with 512 47), with as
-// many as there are groups each pays its start (256 tokens of 128 experts, second product: 135 us, with 512 127).
+// many as there are groups each pays its start (256 tokens of 128 experts, second product: 135 us, with 512 127). Layers of few
+// or narrow experts have fewer groups than that in all, and compute units without work (12 tokens, 4 experts of 4096 x
+// 1024: both products, lists and sums 35 us for 27 MB).
 constexpr int kEnough = 512;
-
 
 template <int F>
 hipError_t launch(const Args &a, bool few, int32_t *list, int4 *where, hipStream_t s) {
